@@ -20,7 +20,8 @@ LOD_ST_BAD_SEQLEN, LOD_ST_BAD_PAGE, LOD_ST_BAD_MEMBER, LOD_ST_BAD_COUNT = 1, 2, 
 # Every symbol include/lod.h declares.
 EXPORTS = ("lod_version", "lod_last_error", "lod_index_sizes", "lod_workspace_bytes",
            "lod_build_index", "lod_build_ready", "lod_append_kv", "lod_decode", "lod_prefill", "lod_get_status",
-           "lod_decode_noalloc")
+           "lod_decode_noalloc", "lod_append_rope", "lod_pool_append", "lod_pool_read",
+           "lod_pool_workspace_bytes", "lod_pool_attend")
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -39,6 +40,25 @@ class lod_index(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("gK", "gV", "gCnt", "pK", "pV", "pCnt", "pBeg", "gPage", "perm", "mK", "mV", "gMeta",
                  "qK", "qV", "qKs", "qVs")]
+
+
+class lod_rope(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("pad", ctypes.c_int32)]
+
+
+class lod_pool(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("bits", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("blocks", ctypes.c_int64), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("Ke", ctypes.c_void_p), ("Ve", ctypes.c_void_p)]
+
+
+class lod_batch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("N", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("new_begin", ctypes.c_void_p)]
 
 
 INDEX_FIELDS = [f for f, _ in lod_index._fields_]
@@ -90,6 +110,19 @@ def load():
     lib.lod_decode_noalloc.restype = ctypes.c_int32
     lib.lod_decode_noalloc.argtypes = [_P(lod_params), _vp, _vp, _vp, _P(_i64), _vp, _P(lod_index), _vp,
                                        _vp, _vp, _vp, _vp, _vp]
+    lib.lod_append_rope.restype = ctypes.c_int32
+    lib.lod_append_rope.argtypes = [_P(lod_params), _P(lod_rope), _vp, _P(_i64), _vp, _vp, _P(_i64), _i64, _vp,
+                                    _vp, _P(_i64), _vp, _vp, _P(_i64), _vp]
+    lib.lod_pool_append.restype = ctypes.c_int32
+    lib.lod_pool_append.argtypes = [_P(lod_pool), _P(lod_batch), _P(lod_rope), _vp, _P(_i64), _vp, _vp, _P(_i64),
+                                    _vp, _P(_i64), _vp, _vp]
+    lib.lod_pool_read.restype = ctypes.c_int32
+    lib.lod_pool_read.argtypes = [_P(lod_pool), _P(lod_batch), _i64, _i64, _vp, _vp, _P(_i64), _vp, _vp]
+    lib.lod_pool_workspace_bytes.restype = ctypes.c_int32
+    lib.lod_pool_workspace_bytes.argtypes = [_P(lod_pool), _P(lod_batch), _P(ctypes.c_size_t)]
+    lib.lod_pool_attend.restype = ctypes.c_int32
+    lib.lod_pool_attend.argtypes = [_P(lod_pool), _P(lod_batch), _vp, _P(_i64), _vp, _P(_i64), _vp, _i64,
+                                    ctypes.c_float, _vp, ctypes.c_size_t, _vp]
     lib.lod_get_status.restype = ctypes.c_int32
     lib.lod_get_status.argtypes = [_vp, _vp, _P(ctypes.c_uint32)]
     _lib = lib

@@ -212,6 +212,224 @@ def lod_prefill(params: Params, q, q_begin: int, K, V, index: Index, out=None, l
     return out
 
 
+# ---------------------------------------------------------------- projections into a cache, block pool
+
+_I2, _I3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
+class Rope:
+    """Norm and rotation of query and key rows (lod_rope).  inv_freq: float32 [rot / 2] on the device (None: no
+    rotation); q_norm, k_norm: [d] weights of the rows' dtype (None: no norm of those rows)."""
+
+    def __init__(self, inv_freq=None, q_norm=None, k_norm=None, interleaved: bool = False, eps: float = 1e-6):
+        if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1
+                                     or not inv_freq.is_contiguous()):
+            raise ValueError("inv_freq must be a contiguous float32 [rot / 2] tensor")
+        for w in (q_norm, k_norm):
+            if w is not None and (w.dim() != 1 or not w.is_contiguous()):
+                raise ValueError("norm weights must be contiguous [d] tensors")
+        self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
+        self._c = _lib.lod_rope(_addr(q_norm), _addr(k_norm), _addr(inv_freq), eps,
+                                0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), 0)
+        self._ref = ctypes.byref(self._c)
+
+    def ref(self, d: int, dtype: torch.dtype):
+        """The C struct, after checking the weights against the rows they are for."""
+        for w in (self.q_norm, self.k_norm):
+            if w is not None and (w.shape[0] != d or w.dtype != dtype):
+                raise ValueError("norm weights must be [%d] %s" % (d, dtype))
+        return self._ref
+
+
+class Pool:
+    """A block pool (lod_pool) over the caller's tensors: K, V [blocks, Hkv, block, d] in dtype, or with Ke, Ve
+    (uint8 [blocks, Hkv, block]) as e4m3 codes (float8_e4m3fn or uint8)."""
+
+    def __init__(self, K, V, Ke=None, Ve=None, *, Hq: int, dtype: torch.dtype):
+        if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or not K.is_contiguous() or not V.is_contiguous():
+            raise ValueError("pool K and V must be contiguous [blocks, Hkv, block, d] of one dtype")
+        if (Ke is None) != (Ve is None):
+            raise ValueError("Ke and Ve go together")
+        if Ke is None:
+            if K.dtype != dtype:
+                raise TypeError("pool dtype %s != %s (8-bit codes need Ke and Ve)" % (K.dtype, dtype))
+        else:
+            if K.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError("8-bit codes must be float8_e4m3fn or uint8, not %s" % K.dtype)
+            for e in (Ke, Ve):
+                if e.shape != K.shape[:3] or e.dtype != torch.uint8 or not e.is_contiguous():
+                    raise ValueError("Ke and Ve must be contiguous uint8 [blocks, Hkv, block]")
+        self.K, self.V, self.Ke, self.Ve, self.dtype, self.Hq = K, V, Ke, Ve, dtype, Hq
+        blocks, self.Hkv, self.block, self.d = K.shape
+        self._c = _lib.lod_pool(_DT[dtype], 0 if Ke is None else 8, Hq, self.Hkv, self.d, self.block, blocks,
+                                _addr(K), _addr(V), _addr(Ke), _addr(Ve))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, blocks: int, block: int, Hq: int, Hkv: int, d: int, dtype: torch.dtype = torch.bfloat16,
+              bits: int = 0, device="cuda") -> "Pool":
+        """A zero-filled pool of its own."""
+        if bits not in (0, 8):
+            raise ValueError("pool bits must be 0 or 8")
+        shape = (blocks, Hkv, block, d)
+        K = torch.zeros(shape, dtype=torch.uint8 if bits else dtype, device=device)
+        e = (lambda: torch.zeros(shape[:3], dtype=torch.uint8, device=device)) if bits else (lambda: None)
+        return cls(K, torch.zeros_like(K), e(), e(), Hq=Hq, dtype=dtype)
+
+    @property
+    def bits(self) -> int:
+        return self._c.bits
+
+
+class PoolBatch:
+    """The sequences of a call (lod_batch): block_table int32 [B, max_blocks], seq_lens int64 [B], new_begin int64
+    [B + 1], all on the device; tokens: packed rows N of the call; max_new: most new tokens of one sequence."""
+
+    def __init__(self, block_table, seq_lens, new_begin=None, tokens: int = 1, max_new: int = 1):
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor")
+        B = block_table.shape[0]
+        if seq_lens.shape != (B,) or seq_lens.dtype != torch.int64 or not seq_lens.is_contiguous():
+            raise ValueError("seq_lens must be a contiguous int64 [B] tensor")
+        if new_begin is not None and (new_begin.shape != (B + 1,) or new_begin.dtype != torch.int64
+                                      or not new_begin.is_contiguous()):
+            raise ValueError("new_begin must be a contiguous int64 [B + 1] tensor")
+        self.block_table, self.seq_lens, self.new_begin = block_table, seq_lens, new_begin
+        self.tokens, self.max_new = tokens, max_new
+        self._c = _lib.lod_batch(B, block_table.shape[1], tokens, max_new, _addr(block_table), _addr(seq_lens),
+                                 _addr(new_begin))
+        self._ref = ctypes.byref(self._c)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, shape, dtype, name):
+    """Strides of rows with contiguous channels (all dimensions but the last)."""
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s; got %s %s" % (name, shape, dtype, tuple(t.shape), t.dtype))
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    return st[:-1]
+
+
+def _stream_handle(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _status_word(status):
+    if status is not None and (status.numel() < 1 or status.element_size() != 4):
+        raise ValueError("status must be a 4-byte integer tensor")
+    return _addr(status)
+
+
+def lod_append_rope(params: Params, rope: Rope, q, k, v, K, V, seq_lens, q_out=None, stream=None):
+    """Append the newest tokens' projections to the dense cache: k, v [B, Hkv, n, d] go to positions
+    [seq_lens - n, seq_lens) of K, V, the keys normed and rotated by `rope`, and the normed and rotated q
+    [B, Hq, n, d] to q_out (which may be q).  q, k, v may be strided views of one fused projection; q None
+    appends the keys and values alone.  Returns q_out."""
+    st = _kv_strides(params, K, V)
+    n = k.shape[2] if k.dim() == 4 else -1
+    ks = _rows(k, (params.B, params.Hkv, n, params.d), params.dtype, "k")
+    if _rows(v, tuple(k.shape), params.dtype, "v") != ks:
+        raise ValueError("k and v must share strides")
+    if seq_lens.shape != (params.B,) or seq_lens.dtype != torch.int64:
+        raise ValueError("seq_lens must be int64 [B]")
+    qs = os = None
+    if q is not None:
+        shape = (params.B, params.Hq, n, params.d)
+        qs = _rows(q, shape, params.dtype, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=q.dtype, device=K.device)
+        os = _I3(*_rows(q_out, shape, params.dtype, "q_out"))
+        qs = _I3(*qs)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    check("lod_append_rope", load().lod_append_rope(
+        ctypes.byref(params.c()), rope.ref(params.d, params.dtype), _addr(q), qs, k.data_ptr(), v.data_ptr(),
+        _I3(*ks), n, K.data_ptr(), V.data_ptr(), st, seq_lens.data_ptr(), _addr(q_out), os,
+        _stream_handle(stream)))
+    return q_out
+
+
+def lod_pool_append(pool: Pool, batch: PoolBatch, k, v, rope: Rope | None = None, q=None, q_out=None, status=None,
+                    stream=None):
+    """Write the new tokens' k, v [N, Hkv, d] into the pool, in its format and normed and rotated by `rope`, and
+    with q [N, Hq, d] the normed and rotated queries to q_out (which may be q).  Returns q_out."""
+    if batch.new_begin is None:
+        raise ValueError("the batch has no new_begin")
+    N, d, dt = batch.tokens, pool.d, pool.dtype
+    ks = _rows(k, (N, pool.Hkv, d), dt, "k")
+    if _rows(v, (N, pool.Hkv, d), dt, "v") != ks:
+        raise ValueError("k and v must share strides")
+    qs = os = None
+    if q is not None:
+        qs = _I2(*_rows(q, (N, pool.Hq, d), dt, "q"))
+        if q_out is None:
+            q_out = torch.empty(N, pool.Hq, d, dtype=dt, device=pool.K.device)
+        os = _I2(*_rows(q_out, (N, pool.Hq, d), dt, "q_out"))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    check("lod_pool_append", load().lod_pool_append(
+        pool._ref, batch._ref, None if rope is None else rope.ref(d, dt), _addr(q), qs, k.data_ptr(), v.data_ptr(),
+        _I2(*ks), _addr(q_out), os, _status_word(status), _stream_handle(stream)))
+    return q_out
+
+
+def lod_pool_read(pool: Pool, batch: PoolBatch, K, V, t_begin: int = 0, t_end: int | None = None, status=None,
+                  stream=None) -> None:
+    """Read tokens [t_begin, min(t_end, seq_lens)) of every sequence into the dense cache K, V [B, Hkv, T, d] of
+    the pool's dtype (t_end None: up to T)."""
+    B = batch.block_table.shape[0]
+    if K.dim() != 4 or K.shape[:2] != (B, pool.Hkv) or K.shape[3] != pool.d or K.shape != V.shape:
+        raise ValueError("K, V must be [B, Hkv, T, d]; got %s / %s" % (tuple(K.shape), tuple(V.shape)))
+    if K.dtype != pool.dtype or V.dtype != pool.dtype:
+        raise TypeError("K/V dtype %s/%s != pool dtype %s" % (K.dtype, V.dtype, pool.dtype))
+    if K.stride() != V.stride() or K.stride(3) != 1:
+        raise ValueError("K and V must share strides with a contiguous last dimension")
+    if t_end is None:
+        t_end = min(K.shape[2], batch.block_table.shape[1] * pool.block)
+    if t_end > K.shape[2]:
+        raise ValueError("t_end %d behind the dense cache's %d tokens" % (t_end, K.shape[2]))
+    check("lod_pool_read", load().lod_pool_read(
+        pool._ref, batch._ref, t_begin, t_end, K.data_ptr(), V.data_ptr(), _I3(*K.stride()[:3]),
+        _status_word(status), _stream_handle(stream)))
+
+
+def pool_workspace_bytes(pool: Pool, batch: PoolBatch) -> int:
+    n = ctypes.c_size_t()
+    check("lod_pool_workspace_bytes", load().lod_pool_workspace_bytes(pool._ref, batch._ref, ctypes.byref(n)))
+    return n.value
+
+
+def pool_workspace(pool: Pool, batch: PoolBatch) -> torch.Tensor:
+    """A zero-filled workspace of lod_pool_attend for this batch."""
+    return torch.zeros(pool_workspace_bytes(pool, batch), dtype=torch.uint8, device=pool.K.device)
+
+
+def lod_pool_attend(pool: Pool, batch: PoolBatch, q, out=None, lse=None, window: int = 0, scale: float = 0.0,
+                    ws=None, stream=None):
+    """Exact causal attention of the new tokens' q [N, Hq, d] over the pool (which already holds them); window > 0
+    limits each query to its last `window` keys; lse float32 [N, Hq].  Returns out."""
+    if batch.new_begin is None:
+        raise ValueError("the batch has no new_begin")
+    shape = (batch.tokens, pool.Hq, pool.d)
+    qs = _I2(*_rows(q, shape, pool.dtype, "q"))
+    if out is None:
+        out = torch.empty(shape, dtype=pool.dtype, device=pool.K.device)
+    os = _I2(*_rows(out, shape, pool.dtype, "out"))
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [N, Hq] tensor")
+    if ws is None:
+        ws = pool_workspace(pool, batch)
+    check("lod_pool_attend", load().lod_pool_attend(
+        pool._ref, batch._ref, q.data_ptr(), qs, out.data_ptr(), os, _addr(lse), window, scale, ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream_handle(stream)))
+    return out
+
+
 def lod_get_status(ws, stream=None) -> int:
     """Read and clear the device status word (LOD_ST_* bits); synchronises."""
     v = ctypes.c_uint32()

@@ -11,11 +11,13 @@
 
 #include <cudaTypedefs.h>
 
+#include "lod_host.cuh"
 #include "lod_internal.cuh"
 
-namespace {
+namespace lod {
+namespace host {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int32_t fail(int32_t code, const char* fmt, ...) {
   va_list ap;
@@ -29,14 +31,12 @@ int32_t cuda_fail(cudaError_t e, const char* what) {
   return fail(LOD_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int32_t ok() {
+  g_err[0] = 0;
+  return LOD_OK;
+}
 
-// A per-call buffer the kernels read or write in place: memory of the current
-// device, managed memory, or page-locked host memory mapped at the same
-// address (cudaHostAlloc / cudaMallocHost under unified addressing: the
-// kernels then move its bytes over the host link themselves).  Pageable host
-// memory and another device's memory are refused before anything is enqueued.
-int32_t check_visible(const void* ptr, const char* name, int* host = nullptr) {
+int32_t check_visible(const void* ptr, const char* name, int* host) {
   if (host) *host = 0;
   if (!ptr) return LOD_OK;
   cudaPointerAttributes at;
@@ -67,6 +67,49 @@ int32_t check_visible_all(std::initializer_list<std::pair<const void*, const cha
   }
   return LOD_OK;
 }
+
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::once_flag g_encode_once;
+
+int32_t encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+                   const cuuint64_t* strides_bytes, cuuint32_t box_rows, CUtensorMapDataType type,
+                   cuuint32_t box_cols) {
+  std::call_once(g_encode_once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return fail(LOD_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t box4[4] = {box_cols, box_rows, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims,
+                        strides_bytes, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(LOD_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return LOD_OK;
+}
+
+static int g_num_sms[64] = {};
+
+int num_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (!g_num_sms[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    g_num_sms[dev] = n;
+  }
+  return g_num_sms[dev];
+}
+
+}  // namespace host
+}  // namespace lod
+
+namespace {
+
+using namespace lod::host;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -203,28 +246,6 @@ AttendShape prefill_shape(const lod_params* p) {
   return s;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-int32_t encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-                   const cuuint64_t* strides_bytes, cuuint32_t box_rows = 128) {
-  std::call_once(g_encode_once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (!g_encode) return fail(LOD_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t box4[4] = {64, box_rows, 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims,
-                        strides_bytes, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(LOD_ECUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
-  return LOD_OK;
-}
-
 // Tensor maps of the group summaries and the KV cache for the tensor-core scan.
 int32_t make_tc_maps(const lod_params* p, const void* K, const void* V, const int64_t* kv, const lod_index* ix,
                      lod::TcMaps* m) {
@@ -307,8 +328,6 @@ PfLayout pf_layout(const lod_params* p) {
   return L;
 }
 
-int g_num_sms[64] = {};
-
 // A second stream of the current device for work that overlaps the caller's
 // stream inside one call (created once per device, never destroyed; it only
 // ever waits on events of the caller's stream).
@@ -327,17 +346,6 @@ int32_t side_stream(cudaStream_t* out) {
   }
   *out = g_side[dev];
   return LOD_OK;
-}
-
-int num_sms() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!g_num_sms[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    g_num_sms[dev] = n;
-  }
-  return g_num_sms[dev];
 }
 
 // Tensor maps of the pair kernel: member-ordered copies and page summaries.
@@ -461,11 +469,20 @@ int32_t do_build(const lod_params* p, const void* K, const void* V, const int64_
 
 }  // namespace
 
+namespace lod {
+namespace host {
+int32_t check_params(const lod_params* p) { return validate(p); }
+int32_t check_cache(const lod_params* p, const void* K, const void* V, const int64_t* kv_strides) {
+  return validate_kv(p, K, V, kv_strides);
+}
+}  // namespace host
+}  // namespace lod
+
 extern "C" {
 
-int32_t lod_version(void) { return 100; }
+int32_t lod_version(void) { return 200; }
 
-const char* lod_last_error(void) { return g_err; }
+const char* lod_last_error(void) { return lod::host::g_err; }
 
 int32_t lod_index_sizes(const lod_params* p, size_t bytes[LOD_INDEX_ARRAYS]) {
   int32_t rc = validate(p);

@@ -1,0 +1,240 @@
+// lod_pool.cuh -- argument blocks, launchers and shared device code of the
+// block pool (append with norm and rotation, read-back, exact attention).
+#pragma once
+
+#include <cuda.h>
+
+#include "lod_internal.cuh"
+
+namespace lod {
+
+// The device side of a lod_batch.
+struct BatchView {
+  const int32_t* table;     // [B][max_blocks]
+  const int64_t* seq_lens;  // [B]
+  const int64_t* begin;     // [B + 1] (null for lod_pool_read)
+  int64_t N, max_new;
+  int B, max_blocks;
+};
+
+// The device side of a lod_pool.
+struct PoolView {
+  void* K;
+  void* V;
+  uint8_t* Ke;
+  uint8_t* Ve;
+  int64_t blocks;
+  int Hkv;
+  int shift;  // log2(block)
+};
+
+struct RopeView {
+  const void* wq;
+  const void* wk;
+  const float* freq;
+  float eps;
+  int rot;
+  int interleaved;
+};
+
+// Rows of new tokens on their way into a cache.
+struct AppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t qb, qh, qt, kb, kh, kt, ob, oh, ot;  // strides in elements (sequence, head, token)
+  int Hq, Hkv;          // Hq = 0: no queries
+  int use_rope;
+  RopeView rope;
+  int64_t N;            // tokens of the call
+  int split;            // warps that share one token's heads
+  // dense cache
+  void* K;
+  void* V;
+  int64_t sb, sh, st, Tmax, n_new;
+  const int64_t* seq_lens;
+  // pool
+  PoolView pool;
+  BatchView batch;
+  uint32_t* status;
+};
+
+struct ReadArgs {
+  PoolView pool;
+  BatchView batch;
+  void* K;
+  void* V;
+  int64_t sb, sh, st, t_begin, t_end;
+  uint32_t* status;
+};
+
+// Exact attention over the pool.  A work unit is (sequence, KV head, tile of
+// TM query rows); row r of a sequence and KV head is query head r % G of its
+// new token r / G.  A unit's keys are cut into tiles of KT; the tiles of all
+// units, in the order sequence, head, row tile, key tile, are one list, and
+// CTA c takes the entries [c * share, (c + 1) * share) of it.
+struct PoolAttendArgs {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t qt, qh, ot, oh;  // strides in elements (token, head)
+  PoolView pool;
+  BatchView batch;
+  int Hq, G;
+  int64_t window;          // 0: none
+  float scale_log2;        // softmax scale * log2 e
+  // workspace
+  uint32_t* status;
+  int64_t* Wb;             // [B + 1] key tiles before each sequence (all heads)
+  int32_t* RT;             // [B + 1] row tiles before each sequence (one head)
+  int32_t* pre;            // [RT[B]] key tiles of the sequence (one head) before each row tile
+  float* part;             // [ctas][2][TM][d] partial sums
+  float2* ml;              // [ctas][2][TM] their (max, sum), log2 units
+  int ctas;
+  int min_share;           // key tiles a CTA takes at least
+  int planned;             // 1: Wb, RT, pre were written by the plan kernel
+};
+
+// Sequence b of a batch, checked: r0 = first packed row, n = new tokens (0
+// when the sequence is refused), len = tokens.
+struct SeqView {
+  int64_t r0, len;
+  int n;
+  bool ok;
+};
+__device__ __forceinline__ SeqView seq_view(const BatchView& bt, int shift, int b) {
+  SeqView s;
+  const int64_t r0 = bt.begin[b], r1 = bt.begin[b + 1];
+  s.len = bt.seq_lens[b];
+  s.r0 = r0;
+  s.ok = r0 >= 0 && r1 >= r0 && r1 <= bt.N && r1 - r0 <= bt.max_new && s.len >= r1 - r0 &&
+         s.len <= ((int64_t)bt.max_blocks << shift);
+  s.n = s.ok ? (int)(r1 - r0) : 0;
+  return s;
+}
+
+// Key tiles [lo, hi) that row tile i (rows [i * TM, ...)) of a sequence reads.
+template <int TM, int KT>
+__device__ __forceinline__ void row_tile_keys(const SeqView& s, int G, int64_t window, int64_t i, int& lo, int& hi) {
+  const int64_t rows = (int64_t)s.n * G;
+  int64_t r1 = (i + 1) * TM;
+  if (r1 > rows) r1 = rows;
+  const int64_t t0 = s.len - s.n + i * TM / G, t1 = s.len - s.n + (r1 - 1) / G;
+  int64_t first = window > 0 ? t0 - window + 1 : 0;
+  if (first < 0) first = 0;
+  lo = (int)(first / KT);
+  hi = (int)(t1 / KT) + 1;
+}
+
+// Unit that holds an entry of the work list, and the entry's key tile.
+struct Unit {
+  int b, h;
+  int64_t i;        // row tile
+  int64_t begin;    // list position of the unit's first key tile
+  int lo, hi;       // its key tiles [lo, hi); entry w is key tile lo + (w - begin)
+};
+
+template <int TM, int KT>
+__device__ __forceinline__ Unit find_unit(const PoolAttendArgs& a, const int64_t* Wb, int64_t w) {
+  Unit u;
+  int lo = 0, hi = a.batch.B;  // Wb[lo] <= w < Wb[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (Wb[mid] <= w) lo = mid; else hi = mid;
+  }
+  u.b = lo;
+  const int64_t per_head = (Wb[lo + 1] - Wb[lo]) / a.pool.Hkv;
+  u.h = (int)((w - Wb[lo]) / per_head);
+  const int64_t head0 = Wb[lo] + u.h * per_head;
+  u.i = 0;
+  u.begin = head0;
+  if (a.planned) {
+    const int32_t* pre = a.pre + a.RT[lo];
+    int64_t l = 0, r = a.RT[lo + 1] - a.RT[lo];
+    while (r - l > 1) {
+      const int64_t mid = (l + r) >> 1;
+      if (pre[mid] <= w - head0) l = mid; else r = mid;
+    }
+    u.i = l;
+    u.begin = head0 + pre[l];
+  }
+  const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
+  row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
+  return u;
+}
+
+// Sequences a CTA can lay out by itself (one row tile each): the list's
+// prefix sums then live in its shared memory and no plan kernel runs.
+constexpr int kInlineSeqs = 256;
+
+// Wb of sequences with one row tile each, by the whole CTA (at least one
+// warp); ends with a CTA barrier.
+template <int TM, int KT>
+__device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb) {
+  if (threadIdx.x < 32) {
+    int64_t at = 0;
+    if (threadIdx.x == 0) Wb[0] = 0;
+    for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
+      const int b = b0 + threadIdx.x;
+      int64_t n = 0;
+      if (b < a.batch.B) {
+        const SeqView s = seq_view(a.batch, a.pool.shift, b);
+        if (s.n > 0) {
+          int lo, hi;
+          row_tile_keys<TM, KT>(s, a.G, a.window, 0, lo, hi);
+          n = (int64_t)(hi - lo) * a.pool.Hkv;
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, n, o);
+        if ((int)threadIdx.x >= o) n += x;
+      }
+      if (b < a.batch.B) Wb[b + 1] = at + n;
+      at += __shfl_sync(0xffffffffu, n, 31);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t total) {
+  const int64_t s = (total + a.ctas - 1) / a.ctas;
+  return s > a.min_share ? s : a.min_share;
+}
+
+// Rows of refused sequences: out = 0, lse = -inf.  Every CTA of the grid calls
+// this with all its threads; the CTAs share the sequences out.
+template <typename T, int D>
+__device__ __forceinline__ void clear_refused(const PoolAttendArgs& a) {
+  constexpr int N16 = D * (int)sizeof(T) / 16;
+  for (int b = blockIdx.x; b < a.batch.B; b += gridDim.x) {
+    const SeqView s = seq_view(a.batch, a.pool.shift, b);
+    if (s.ok) continue;
+    if (threadIdx.x == 0) set_status(a.status, LOD_ST_BAD_SEQLEN);
+    int64_t r0 = a.batch.begin[b], r1 = a.batch.begin[b + 1];
+    if (r0 < 0) r0 = 0;
+    if (r1 > a.batch.N) r1 = a.batch.N;
+    for (int64_t x = threadIdx.x; r0 < r1 && x < (r1 - r0) * a.Hq * N16; x += blockDim.x) {
+      const int64_t row = x / N16, t = r0 + row / a.Hq, h = row % a.Hq;
+      const int c = (int)(x % N16);
+      reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.ot + h * a.oh)[c] = make_uint4(0, 0, 0, 0);
+      if (c == 0 && a.lse) a.lse[t * a.Hq + h] = -INFINITY;
+    }
+  }
+}
+
+cudaError_t launch_append_rows(const AppendArgs& a, int dtype, int d, bool pool, int bits, cudaStream_t stream);
+cudaError_t launch_pool_read(const ReadArgs& a, int dtype, int bits, int d, cudaStream_t stream);
+
+// Shape of an attention call: which kernel, its tiles and its CTAs.
+struct PoolShape {
+  int kind;  // 0: CUDA cores
+  int TM, KT, ctas;
+  bool inline_plan;
+  size_t off_plan, off_ml, off_part, total;  // workspace offsets
+};
+PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms);
+cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, int dtype, int bits, int d, cudaStream_t stream);
+
+}  // namespace lod

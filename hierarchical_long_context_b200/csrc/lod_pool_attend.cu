@@ -1,0 +1,426 @@
+// lod_pool_attend.cu -- exact attention of new tokens over the block pool: the
+// work list, the CUDA-core kernel and the merge of a unit's pieces.
+#include <cuda_fp8.h>
+
+#include "lod_pool.cuh"
+
+namespace lod {
+namespace {
+
+// ---------------------------------------------------------------- work list
+
+// Inclusive scan of one value per thread over the CTA (1024 threads);
+// `total` receives the sum.
+__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    int64_t s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  if (w > 0) v += warp_sums[w - 1];
+  *total = warp_sums[31];
+  __syncthreads();
+  return v;
+}
+
+// Prefix sums of the work list, for sequences with several row tiles: one CTA,
+// a warp per sequence for the sums inside it.
+template <int TM, int KT>
+__global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
+  __shared__ int64_t ws[32];
+  const int B = a.batch.B, lane = threadIdx.x & 31;
+  int64_t at = 0, total;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0;
+    if (b < B) n = ((int64_t)seq_view(a.batch, a.pool.shift, b).n * a.G + TM - 1) / TM;
+    const int64_t s = block_scan(n, ws, &total);
+    if (b < B) a.RT[b + 1] = (int32_t)(at + s);
+    at += total;
+  }
+  if (threadIdx.x == 0) a.RT[0] = 0;
+  __syncthreads();
+  for (int b = threadIdx.x >> 5; b < B; b += 32) {
+    const SeqView s = seq_view(a.batch, a.pool.shift, b);
+    const int64_t rt = a.RT[b];
+    const int64_t nt = a.RT[b + 1] - rt;
+    int64_t sum = 0;
+    for (int64_t i0 = 0; i0 < nt; i0 += 32) {
+      const int64_t i = i0 + lane;
+      int64_t n = 0;
+      if (i < nt) {
+        int lo, hi;
+        row_tile_keys<TM, KT>(s, a.G, a.window, i, lo, hi);
+        n = hi - lo;
+      }
+      int64_t v = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (i < nt) a.pre[rt + i] = (int32_t)(sum + v - n);
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) a.Wb[b + 1] = sum * a.pool.Hkv;
+  }
+  __syncthreads();
+  at = 0;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    const int64_t s = block_scan(b < B ? a.Wb[b + 1] : 0, ws, &total);
+    if (b < B) a.Wb[b + 1] = at + s;
+    at += total;
+  }
+  if (threadIdx.x == 0) a.Wb[0] = 0;
+}
+
+// ---------------------------------------------------------------- CUDA cores
+
+// fp32 attention on the CUDA cores.  A CTA of 4 * TM threads (128 at least)
+// holds a tile of TM query rows; per 64-key tile S = Q K^T and O += P V from
+// shared memory, each thread RPT rows x 4 keys of S and the same rows x D/16
+// channels of O, so 16 neighbouring lanes own a row and its maximum and sum
+// need no shared memory.  fp32 has no tensor-core form of its own accuracy,
+// so FFMA bounds it; per 4 channels a thread reads RPT + 4 vectors for 16 RPT
+// FMAs.
+template <typename T, int D, int TM, bool Q8>
+__global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAttendArgs a) {
+  constexpr int KT = 64, NT = TM == 16 ? 128 : 256, RPT = TM * 16 / NT, CPT = D / 16;
+  constexpr int KS = D + 4, PS = KT + 4;
+  constexpr int E = 16 / (int)sizeof(T), PPR = D / E;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;               // [TM][D]
+  float* Ks = Qs + TM * D;      // [KT][KS]
+  float* Vs = Ks + KT * KS;     // [KT][D]
+  float* Ps = Vs + KT * D;      // [TM][PS]
+  int* live = reinterpret_cast<int*>(Ps + TM * PS);  // [KT]: the key exists
+  __shared__ int64_t wb_s[kInlineSeqs + 1];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+
+  const int64_t* Wb = a.Wb;
+  if (!a.planned) {
+    plan_inline<TM, KT>(a, wb_s);
+    Wb = wb_s;
+  }
+  clear_refused<T, D>(a);
+  const int64_t total = Wb[a.batch.B], share = list_share(a, total);
+  const int64_t w0 = blockIdx.x * share, w1 = w0 + share < total ? w0 + share : total;
+
+  for (int64_t w = w0; w < w1;) {
+    const Unit u = find_unit<TM, KT>(a, Wb, w);
+    const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
+    const int64_t uend = u.begin + (u.hi - u.lo);
+    const int64_t pe = uend < w1 ? uend : w1;
+    const int kt0 = u.lo + (int)(w - u.begin), kt1 = u.lo + (int)(pe - u.begin);
+    const int64_t row0 = u.i * TM, rows = (int64_t)s.n * a.G;
+    const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
+    const int32_t* table = a.batch.table + (int64_t)u.b * a.batch.max_blocks;
+
+    __syncthreads();
+    for (int x = tid; x < TM * PPR; x += NT) {
+      const int r = x / PPR, c = x % PPR;
+      float v[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = 0.f;
+      if (r < nrow) {
+        const int64_t g = row0 + r;
+        const T* q = static_cast<const T*>(a.q) + (s.r0 + g / a.G) * a.qt + (u.h * a.G + g % a.G) * a.qh;
+        load_f<T, E>(q + c * E, v);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) Qs[r * D + c * E + i] = v[i];
+    }
+    float m[RPT], l[RPT], acc[RPT][CPT];
+    int64_t pos[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = ty * RPT + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      pos[i] = r < nrow ? s.len - s.n + (row0 + r) / a.G : -1;
+#pragma unroll
+      for (int j = 0; j < CPT; ++j) acc[i][j] = 0.f;
+    }
+    for (int kt = kt0; kt < kt1; ++kt) {
+      __syncthreads();
+      for (int x = tid; x < KT * PPR; x += NT) {
+        const int k = x / PPR, c = x % PPR;
+        const int64_t t = (int64_t)kt * KT + k;
+        int64_t blk = -1;
+        if (t < s.len) {
+          blk = table[t >> a.pool.shift];
+          if (blk < 0 || blk >= a.pool.blocks) {
+            blk = -1;
+            set_status(a.status, LOD_ST_BAD_PAGE);
+          }
+        }
+        if (c == 0) live[k] = blk >= 0;
+        float kv[2][E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) kv[0][i] = kv[1][i] = 0.f;
+        if (blk >= 0) {
+          const int64_t row = ((blk * a.pool.Hkv + u.h) << a.pool.shift) + (t & (((int64_t)1 << a.pool.shift) - 1));
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const void* base = z ? a.pool.V : a.pool.K;
+            if constexpr (!Q8) {
+              load_f<T, E>(static_cast<const T*>(base) + row * D + c * E, kv[z]);
+            } else {
+              const uint8_t* src = static_cast<const uint8_t*>(base) + row * D + c * E;
+              const int E8 = (z ? a.pool.Ve : a.pool.Ke)[row];
+              const float f = E8 == 255 ? NAN : E8 == 0 ? __uint_as_float(0x400000u) : __uint_as_float((uint32_t)E8 << 23);
+#pragma unroll
+              for (int i = 0; i < E / 4; ++i) {
+                const uint32_t word = reinterpret_cast<const uint32_t*>(src)[i];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const __half2_raw hr =
+                      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * j)), __NV_E4M3);
+                  const float2 f2 = __half22float2(__half2(hr));
+                  kv[z][4 * i + 2 * j] = f2.x * f;
+                  kv[z][4 * i + 2 * j + 1] = f2.y * f;
+                }
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          Ks[k * KS + c * E + i] = kv[0][i];
+          Vs[k * D + c * E + i] = kv[1][i];
+        }
+      }
+      __syncthreads();
+      // S: rows ty * RPT + i, keys tx + 16 j
+      float sc[RPT][4];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
+#pragma unroll 4
+      for (int e = 0; e < D; e += 4) {
+        float4 kk[4], qq[RPT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * j) * KS + e]);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) qq[i] = *reinterpret_cast<const float4*>(&Qs[(ty * RPT + i) * D + e]);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sc[i][j] = fmaf(qq[i].x, kk[j].x,
+                            fmaf(qq[i].y, kk[j].y, fmaf(qq[i].z, kk[j].z, fmaf(qq[i].w, kk[j].w, sc[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = tx + 16 * j;
+          const int64_t t = (int64_t)kt * KT + k;
+          const bool seen = live[k] && t <= pos[i] && (a.window <= 0 || t > pos[i] - a.window);
+          sc[i][j] = seen ? sc[i][j] * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, sc[i][j]);
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[i], mx);
+        const float ref = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
+        const float f = exp2f(m[i] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(sc[i][j] - ref);
+          sum += p;
+          Ps[(ty * RPT + i) * PS + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = fmaf(l[i], f, sum);
+        m[i] = mn;
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) acc[i][j] *= f;
+      }
+      __syncwarp();  // a row's weights are written and read by one half warp
+#pragma unroll 2
+      for (int k = 0; k < KT; k += 4) {
+        float4 pp[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) pp[i] = *reinterpret_cast<const float4*>(&Ps[(ty * RPT + i) * PS + k]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+#pragma unroll
+          for (int c = 0; c < CPT / 4; ++c) {
+            const float4 vv = *reinterpret_cast<const float4*>(&Vs[(k + z) * D + c * 64 + tx * 4]);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+              const float p = z == 0 ? pp[i].x : z == 1 ? pp[i].y : z == 2 ? pp[i].z : pp[i].w;
+              acc[i][4 * c + 0] = fmaf(p, vv.x, acc[i][4 * c + 0]);
+              acc[i][4 * c + 1] = fmaf(p, vv.y, acc[i][4 * c + 1]);
+              acc[i][4 * c + 2] = fmaf(p, vv.z, acc[i][4 * c + 2]);
+              acc[i][4 * c + 3] = fmaf(p, vv.w, acc[i][4 * c + 3]);
+            }
+          }
+        }
+      }
+    }
+    // the unit's result, or this CTA's piece of it
+    const bool whole = w == u.begin && pe == uend;
+    const int slot = 2 * blockIdx.x + (u.begin >= w0 ? 1 : 0);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = ty * RPT + i;
+      if (r >= nrow) continue;
+      const int64_t g = row0 + r, tok = s.r0 + g / a.G, head = u.h * a.G + g % a.G;
+      if (whole) {
+        const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;
+        T* o = static_cast<T*>(a.out) + tok * a.ot + head * a.oh;
+#pragma unroll
+        for (int c = 0; c < CPT / 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[c * 64 + tx * 4 + j] = Elem<T>::from_f(acc[i][4 * c + j] * inv);
+        if (tx == 0 && a.lse) a.lse[tok * a.Hq + head] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
+      } else {
+        float* o = a.part + ((int64_t)slot * TM + r) * D;
+#pragma unroll
+        for (int c = 0; c < CPT / 4; ++c)
+          *reinterpret_cast<float4*>(o + c * 64 + tx * 4) =
+              make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
+        if (tx == 0) a.ml[(int64_t)slot * TM + r] = make_float2(m[i], l[i]);
+      }
+    }
+    w = pe;
+  }
+}
+
+// ---------------------------------------------------------------- merge
+
+// Joins the pieces of the unit that begins in CTA c's part of the list and
+// ends behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
+// in that order, so the result does not depend on which CTA ran when.  One
+// warp per row, blockIdx.y picks 16 rows.
+template <typename T, int D, int TM, int KT>
+__global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
+  __shared__ int64_t wb_s[kInlineSeqs + 1];
+  const int64_t* Wb = a.Wb;
+  if (!a.planned) {
+    plan_inline<TM, KT>(a, wb_s);
+    Wb = wb_s;
+  }
+  const int64_t total = Wb[a.batch.B], share = list_share(a, total);
+  const int64_t w0 = blockIdx.x * share, w1 = w0 + share;
+  if (w1 >= total) return;
+  const Unit u = find_unit<TM, KT>(a, Wb, w1 - 1);
+  const int64_t uend = u.begin + (u.hi - u.lo);
+  if (u.begin < w0 || uend <= w1) return;
+  const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
+  const int64_t rows = (int64_t)s.n * a.G, row0 = u.i * TM;
+  const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
+  const int pieces = (int)((uend - 1) / share) - (int)blockIdx.x + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int C = D / 32;
+  auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  for (int r = blockIdx.y * 16 + warp; r < nrow && r < (int)blockIdx.y * 16 + 16; r += 8) {
+    float m = -INFINITY;
+    bool bad = false;  // NaN goes through the maximum unseen
+    for (int i = lane; i < pieces; i += 32) {
+      const float x = a.ml[slot(i) * TM + r].x;
+      m = fmaxf(m, x);
+      bad |= x != x;
+    }
+    m = warp_max(m);
+    if (__any_sync(0xffffffffu, bad)) m = NAN;
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const int64_t at = slot(i) * TM + r;
+      const float2 x = a.ml[at];
+      const float f = exp2f(x.x - ref);
+      l = fmaf(x.y, f, l);
+      const float* p = a.part + at * D + lane * C;
+#pragma unroll
+      for (int j = 0; j < C; ++j) o[j] = fmaf(p[j], f, o[j]);
+    }
+    const int64_t g = row0 + r, tok = s.r0 + g / a.G, head = u.h * a.G + g % a.G;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    T* out = static_cast<T*>(a.out) + tok * a.ot + head * a.oh + lane * C;
+#pragma unroll
+    for (int j = 0; j < C; ++j) out[j] = Elem<T>::from_f(o[j] * inv);
+    if (lane == 0 && a.lse) a.lse[tok * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <int TM, int KT>
+cudaError_t launch_plan(const PoolAttendArgs& a, cudaStream_t st) {
+  pool_plan_kernel<TM, KT><<<1, 1024, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int TM, int KT>
+cudaError_t launch_merge(const PoolAttendArgs& a, cudaStream_t st) {
+  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas, (TM + 15) / 16), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int TM, bool Q8>
+cudaError_t launch_simt(const PoolAttendArgs& a, cudaStream_t st) {
+  constexpr int KT = 64;
+  constexpr size_t smem = sizeof(float) * (TM * D + KT * (D + 4) + KT * D + TM * (KT + 4)) + sizeof(int) * KT;
+  cudaError_t e = set_smem_once<pool_simt_kernel<T, D, TM, Q8>>(smem);
+  if (e == cudaSuccess && a.planned) e = launch_plan<TM, KT>(a, st);
+  if (e != cudaSuccess) return e;
+  pool_simt_kernel<T, D, TM, Q8><<<a.ctas, TM == 16 ? 128 : 256, smem, st>>>(a);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_merge<T, D, TM, KT>(a, st);
+}
+
+template <typename T, int D>
+cudaError_t launch_simt_d(const PoolAttendArgs& a, int TM, int bits, cudaStream_t st) {
+  if (TM == 16) return bits == 8 ? launch_simt<T, D, 16, true>(a, st) : launch_simt<T, D, 16, false>(a, st);
+  return bits == 8 ? launch_simt<T, D, 64, true>(a, st) : launch_simt<T, D, 64, false>(a, st);
+}
+
+}  // namespace
+
+PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms) {
+  PoolShape s = {};
+  s.kind = 0;
+  s.TM = max_new * G <= 16 ? 16 : 64;
+  s.KT = 64;
+  s.ctas = sms * 2;
+  s.inline_plan = max_new * G <= s.TM && B <= kInlineSeqs;
+  const int64_t tiles = N * G / s.TM + B;
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  s.off_plan = kWsHeader;
+  size_t plan = s.inline_plan ? 0 : (size_t)(B + 1) * 16 + (size_t)tiles * 4;
+  s.off_ml = s.off_plan + up(plan);
+  s.off_part = s.off_ml + up((size_t)s.ctas * 2 * s.TM * sizeof(float2));
+  s.total = s.off_part + up((size_t)s.ctas * 2 * s.TM * d * sizeof(float));
+  return s;
+}
+
+cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, int dtype, int bits, int d, cudaStream_t stream) {
+  if (dtype == LOD_DTYPE_F32)
+    return d == 64 ? launch_simt_d<float, 64>(a, s.TM, bits, stream) : launch_simt_d<float, 128>(a, s.TM, bits, stream);
+  return d == 64 ? launch_simt_d<__nv_bfloat16, 64>(a, s.TM, bits, stream)
+                 : launch_simt_d<__nv_bfloat16, 128>(a, s.TM, bits, stream);
+}
+
+}  // namespace lod

@@ -339,6 +339,175 @@ int32_t lod_decode_noalloc(const lod_params* p, const void* q, const void* K, co
                            void* out, float* lse, int32_t* sel_groups, int32_t* sel_pages,
                            uint32_t* status, lod_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Writing projections into a cache, and the block pool.
+ *
+ * lod_append_rope takes a layer's query, key and value projections of the
+ * newest tokens to the dense cache of lod_decode and lod_prefill: per-head
+ * norm and position rotation in the pass that writes the cache.  A block pool
+ * keeps the keys and values of many sequences in fixed-size blocks, in the
+ * model's dtype or in 8 bits: lod_pool_append writes it (with the same norm
+ * and rotation), lod_pool_attend is exact attention of the newest tokens over
+ * it, and lod_pool_read brings a sequence back into the dense cache, where
+ * lod_build_index, lod_decode and lod_prefill take it.
+ * --------------------------------------------------------------------- */
+
+/*
+ * Norm and rotation of query and key rows (one row = one token's one head, d
+ * channels).  With x the row in fp32:
+ *   norm      y = x / sqrt(mean(x^2) + eps) * w, where q_norm / k_norm give w
+ *             (device [d], the call's dtype, 16-byte aligned); y = x where
+ *             that pointer is NULL
+ *   rotation  the first rot channels (even, 0 <= rot <= d) in rot/2 pairs
+ *             (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a), a =
+ *             position * inv_freq[i] for pair i (device [rot/2] float), the
+ *             product and its reduction taken in 64 bits; pair i is channels
+ *             (i, i + rot/2), or (2i, 2i + 1) with interleaved = 1
+ * Everything is computed in fp32 and rounded once, to the type it is stored in.
+ */
+typedef struct lod_rope {
+  const void* q_norm;
+  const void* k_norm;
+  const float* inv_freq; /* may be NULL when rot = 0 */
+  float eps;             /* >= 0 */
+  int32_t rot;
+  int32_t interleaved;
+  int32_t pad;           /* 0 */
+} lod_rope;
+
+/*
+ * Append the n_new newest tokens of every sequence to the dense cache: token
+ * i of sequence b sits at position t = seq_lens[b] - n_new + i (seq_lens as
+ * for lod_append_kv: the length after the append, device [B] int64).  Its
+ * normed and rotated key rows and its value rows go to K/V[b][h][t], its
+ * normed and rotated query rows to q_out.
+ *   q        device, p->dtype, [B][Hq][n_new][d] with element strides
+ *            q_strides = {b, h, token}
+ *   k, v     device, p->dtype, [B][Hkv][n_new][d] with the strides
+ *            kv_new_strides; views of one fused projection are fine
+ *   q_out    device [B][Hq][n_new][d] with strides q_out_strides; it may be q
+ *            itself (same strides).  q and q_out are both NULL to append k
+ *            and v alone.
+ * Innermost channels are contiguous; pointers and strides are 16-byte
+ * aligned.  The buffers above may be page-locked host memory.  A sequence
+ * whose length is below n_new or above Tmax is skipped (cache and q_out left
+ * as they were).
+ */
+int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q, const int64_t q_strides[3],
+                        const void* k, const void* v, const int64_t kv_new_strides[3], int64_t n_new, void* K,
+                        void* V, const int64_t kv_strides[3], const int64_t* seq_lens, void* q_out,
+                        const int64_t q_out_strides[3], lod_stream_t stream);
+
+/*
+ * A block pool: `blocks` blocks of `block` tokens each,
+ *   K, V     device [blocks][Hkv][block][d]
+ *   Ke, Ve   device [blocks][Hkv][block] uint8, bits = 8 only (else NULL)
+ * bits = 0: rows hold dtype.  bits = 8: rows hold e4m3 codes c_i and one
+ * exponent byte E, and a row reads c_i * 2^(E - 127).  It is written with the
+ * least integer e = E - 127 for which max|x| <= 448 * 2^e, clamped to
+ * [-120, 119], and c_i = x_i * 2^-e rounded to nearest even (saturated at
+ * 448).  Scaling by a power of two is exact, so a row's only rounding is that
+ * of its codes, and a row reads back exactly in bf16.  A row that holds an
+ * infinity or NaN is stored with E = 255 and reads NaN in every channel.
+ * Supported: dtype F32 or BF16, bits 0 or 8, d in {64, 128}, block in
+ * {16, 32, 64, 128}, Hq a multiple of Hkv with Hq/Hkv <= 64, blocks * Hkv *
+ * block < 2^31.  K and V are 16-byte aligned device memory.
+ */
+typedef struct lod_pool {
+  int32_t dtype; /* lod_dtype: q, k, v and out, and the rows with bits = 0 */
+  int32_t bits;
+  int32_t Hq;
+  int32_t Hkv;
+  int32_t d;
+  int32_t block;
+  int64_t blocks;
+  void* K;
+  void* V;
+  uint8_t* Ke;
+  uint8_t* Ve;
+} lod_pool;
+
+/*
+ * The sequences of one call.  Tokens of all sequences are packed: sequence
+ * b's new tokens are rows [new_begin[b], new_begin[b + 1]) of the call's N,
+ * the last of its seq_lens[b] tokens; token t of a sequence lives in block
+ * block_table[b][t / block] at row t % block.
+ * The device values are checked by the kernels: a sequence with new_begin
+ * outside 0 <= new_begin[b] <= new_begin[b + 1] <= N, more than max_new new
+ * tokens, fewer tokens than new tokens, or more than max_blocks * block
+ * tokens is refused (LOD_ST_BAD_SEQLEN); a table entry outside [0, blocks) is
+ * never followed (LOD_ST_BAD_PAGE).  Entries behind a sequence's last block
+ * are not read.  Sequences without new tokens are fine, and so are rows of
+ * the N that no sequence owns: they are left as they were.  Two new tokens
+ * must not share a place in the pool.
+ */
+typedef struct lod_batch {
+  int32_t B;                  /* sequences, 1 .. 65535 */
+  int32_t max_blocks;         /* entries of one row of block_table, >= 1 */
+  int64_t N;                  /* packed rows, >= 1 */
+  int64_t max_new;            /* most new tokens of one sequence, 1 .. N */
+  const int32_t* block_table; /* device [B][max_blocks] */
+  const int64_t* seq_lens;    /* device [B]: tokens, the new ones included */
+  const int64_t* new_begin;   /* device [B + 1] */
+} lod_batch;
+
+/*
+ * Write the new tokens' keys and values into the pool, normed and rotated by
+ * `rope` (NULL: as they are) and in the pool's format; with q, also the
+ * normed and rotated queries to q_out (both NULL: keys and values alone; q
+ * needs rope).
+ *   q        device [N][Hq][d] with element strides q_strides = {token, head}
+ *   k, v     device [N][Hkv][d] with the strides kv_new_strides
+ *   q_out    device [N][Hq][d] with strides q_out_strides; may be q itself
+ *   status   nullable device word (4-byte aligned) that receives (bitwise OR)
+ *            this call's LOD_ST_* bits; the caller zeroes it
+ * A refused sequence writes nothing, a token whose block entry is bad writes
+ * only its q_out.  The buffers above and new_begin, seq_lens and block_table
+ * may be page-locked host memory.
+ */
+int32_t lod_pool_append(const lod_pool* pool, const lod_batch* batch, const lod_rope* rope, const void* q,
+                        const int64_t q_strides[2], const void* k, const void* v, const int64_t kv_new_strides[2],
+                        void* q_out, const int64_t q_out_strides[2], uint32_t* status, lod_stream_t stream);
+
+/*
+ * Read tokens [t_begin, min(t_end, seq_lens[b])) of every sequence from the
+ * pool into a dense cache K, V of the pool's dtype, rows K[b][h][t] as in
+ * lod_build_index (strides kv_strides = {b, h, token} in elements; the dense
+ * rows [t_begin, t_end) must exist).  batch->N, max_new and new_begin are
+ * not read.  Other rows are left as they were, as are those of a refused
+ * sequence and of a bad block.  status as for lod_pool_append.
+ */
+int32_t lod_pool_read(const lod_pool* pool, const lod_batch* batch, int64_t t_begin, int64_t t_end, void* K,
+                      void* V, const int64_t kv_strides[3], uint32_t* status, lod_stream_t stream);
+
+/*
+ * Workspace bytes of lod_pool_attend for a batch of at most batch->B
+ * sequences, N rows and max_new new tokens of one sequence (device pointers
+ * of pool and batch are not looked at).  256-byte aligned device memory,
+ * zeroed once after allocation; its first word is the status word of
+ * lod_get_status.
+ */
+int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, size_t* bytes);
+
+/*
+ * Exact causal attention of the new tokens over the pool, which already holds
+ * them: the query of a token at position t sees keys j of its sequence with
+ * j <= t and, where window > 0, j > t - window.
+ *   q        device [N][Hq][d], pool dtype, element strides q_strides = {token, head}
+ *   out      device [N][Hq][d], strides out_strides; rounded once from fp32
+ *            (with bf16 the softmax weights are rounded to bf16 before they
+ *            meet the values)
+ *   lse      device [N][Hq] float log-sum-exp (nullable)
+ *   scale    softmax scale; <= 0 means 1/sqrt(d)
+ * Values stored at positions below a sequence's length must be finite unless
+ * a NaN result is meant; what a block holds behind the length is never used.
+ * Keys in a bad block are left out; a row that sees no key then, and every
+ * row of a refused sequence that lies in [0, N), gets out = 0 and lse = -inf.
+ */
+int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void* q, const int64_t q_strides[2],
+                        void* out, const int64_t out_strides[2], float* lse, int64_t window, float scale, void* ws,
+                        size_t ws_bytes, lod_stream_t stream);
+
 /*
  * Read and clear the device status word kept in `ws` (the only synchronising
  * call: it waits for `stream`).  *status (host) receives the LOD_ST_* bits
