@@ -164,6 +164,61 @@ __device__ __forceinline__ Unit find_unit(const PoolAttendArgs& a, const int64_t
   return u;
 }
 
+// A CTA's walk through its part [w, w1) of the list, one piece of a unit at a
+// time: key tiles [kt0, kt1) of unit u.  Every role of a CTA takes the same walk.
+template <int TM, int KT>
+struct Walk {
+  const PoolAttendArgs& a;
+  int64_t w0, w, w1, uend;
+  Unit u;
+  SeqView s;
+  int nt, kt0, kt1, nrow;
+
+  __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* Wb, int cta) : a(args) {
+    const int64_t total = Wb[a.batch.B];
+    int64_t share = (total + a.ctas - 1) / a.ctas;
+    if (share < a.min_share) share = a.min_share;
+    w0 = w = cta * share;
+    w1 = w0 + share < total ? w0 + share : total;
+    if (w < w1) {
+      u = find_unit<TM, KT>(a, Wb, w);
+      s = seq_view(a.batch, a.pool.shift, u.b);
+      nt = (s.n * a.G + TM - 1) / TM;
+      piece();
+    }
+  }
+  __device__ __forceinline__ bool more() const { return w < w1; }
+  __device__ __forceinline__ void piece() {
+    uend = u.begin + (u.hi - u.lo);
+    const int64_t pe = uend < w1 ? uend : w1;
+    kt0 = u.lo + (int)(w - u.begin);
+    kt1 = u.lo + (int)(pe - u.begin);
+    const int left = s.n * a.G - (int)u.i * TM;
+    nrow = left < TM ? left : TM;
+  }
+  __device__ __forceinline__ void next() {
+    w += kt1 - kt0;
+    if (w >= w1) return;
+    u.begin = uend;  // a piece that does not reach its unit's end is the walk's last
+    if (u.i + 1 < nt) {
+      ++u.i;
+    } else {
+      u.i = 0;
+      if (++u.h == a.pool.Hkv) {
+        u.h = 0;
+        do {
+          s = seq_view(a.batch, a.pool.shift, ++u.b);
+        } while (s.n == 0);
+        nt = (s.n * a.G + TM - 1) / TM;
+      }
+    }
+    row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
+    piece();
+  }
+  __device__ __forceinline__ bool whole() const { return w == u.begin && w + (kt1 - kt0) == uend; }
+  __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (u.begin >= w0 ? 1 : 0); }
+};
+
 // Sequences a CTA can lay out by itself (one row tile each): the list's
 // prefix sums then live in its shared memory and no plan kernel runs.
 constexpr int kInlineSeqs = 256;
@@ -229,12 +284,20 @@ cudaError_t launch_pool_read(const ReadArgs& a, int dtype, int bits, int d, cuda
 
 // Shape of an attention call: which kernel, its tiles and its CTAs.
 struct PoolShape {
-  int kind;  // 0: CUDA cores
+  int kind;  // 0: CUDA cores; 1: tensor cores, 256 rows a unit
   int TM, KT, ctas;
   bool inline_plan;
   size_t off_plan, off_ml, off_part, total;  // workspace offsets
 };
 PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms);
-cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, int dtype, int bits, int d, cudaStream_t stream);
+// TMA tensor maps of a bf16 pool's K and V: rows x d, boxes of 64 channels x one block.
+struct __align__(64) PoolMaps {
+  CUtensorMap K, V;
+};
+// Tensor cores, many rows: bf16 rows or e4m3 codes.
+cudaError_t launch_pool_rows(const PoolAttendArgs& a, const PoolMaps* maps, int bits, int d, cudaStream_t stream);
+
+cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, const PoolMaps* maps, int dtype, int bits, int d,
+                               cudaStream_t stream);
 
 }  // namespace lod

@@ -61,6 +61,8 @@ int32_t check_pool(const lod_pool* p) {
   if (!p->K || !p->V) return fail(LOD_EINVAL, "pool K and V must be non-NULL");
   if (!aligned16(p->K) || !aligned16(p->V)) return fail(LOD_EINVAL, "pool K and V must be 16-byte aligned");
   if (p->bits == 8 && (!p->Ke || !p->Ve)) return fail(LOD_EINVAL, "an 8-bit pool needs Ke and Ve");
+  if (p->bits == 8 && (!aligned16(p->Ke) || !aligned16(p->Ve)))
+    return fail(LOD_EINVAL, "pool Ke and Ve must be 16-byte aligned");
   return check_visible_all({{p->K, "pool K"}, {p->V, "pool V"}, {p->bits == 8 ? p->Ke : nullptr, "pool Ke"},
                             {p->bits == 8 ? p->Ve : nullptr, "pool Ve"}});
 }
@@ -301,7 +303,16 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
   a.part = reinterpret_cast<float*>(w + s.off_part);
   a.ctas = s.ctas;
   a.min_share = 1;
-  const cudaError_t e = lod::launch_pool_attend(a, s, pool->dtype, pool->bits, pool->d, (cudaStream_t)stream);
+  lod::PoolMaps maps;
+  const bool tma = s.kind == 1 && pool->bits == 0;
+  if (tma) {
+    const cuuint64_t dims[2] = {(cuuint64_t)pool->d, (cuuint64_t)(pool->blocks * pool->Hkv * pool->block)};
+    const cuuint64_t row[1] = {(cuuint64_t)pool->d * 2};
+    rc = encode_map(&maps.K, pool->K, 2, dims, row, pool->block);
+    if (!rc) rc = encode_map(&maps.V, pool->V, 2, dims, row, pool->block);
+    if (rc) return rc;
+  }
+  const cudaError_t e = lod::launch_pool_attend(a, s, tma ? &maps : nullptr, pool->dtype, pool->bits, pool->d, (cudaStream_t)stream);
   return e != cudaSuccess ? cuda_fail(e, "pool attend launch") : ok();
 }
 

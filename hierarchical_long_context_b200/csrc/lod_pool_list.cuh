@@ -1,0 +1,164 @@
+// lod_pool_list.cuh -- kernels around every attention kernel of the block pool:
+// the prefix sums of its work list and the merge of the units' pieces.
+#pragma once
+
+#include "lod_pool.cuh"
+
+namespace lod {
+namespace {
+
+// ---------------------------------------------------------------- work list
+
+// Inclusive scan of one value per thread over the CTA (1024 threads);
+// `total` receives the sum.
+__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    int64_t s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  if (w > 0) v += warp_sums[w - 1];
+  *total = warp_sums[31];
+  __syncthreads();
+  return v;
+}
+
+// Prefix sums of the work list, for sequences with several row tiles: one CTA,
+// a warp per sequence for the sums inside it.
+template <int TM, int KT>
+__global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
+  __shared__ int64_t ws[32];
+  const int B = a.batch.B, lane = threadIdx.x & 31;
+  int64_t at = 0, total;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    int64_t n = 0;
+    if (b < B) n = ((int64_t)seq_view(a.batch, a.pool.shift, b).n * a.G + TM - 1) / TM;
+    const int64_t s = block_scan(n, ws, &total);
+    if (b < B) a.RT[b + 1] = (int32_t)(at + s);
+    at += total;
+  }
+  if (threadIdx.x == 0) a.RT[0] = 0;
+  __syncthreads();
+  for (int b = threadIdx.x >> 5; b < B; b += 32) {
+    const SeqView s = seq_view(a.batch, a.pool.shift, b);
+    const int64_t rt = a.RT[b];
+    const int64_t nt = a.RT[b + 1] - rt;
+    int64_t sum = 0;
+    for (int64_t i0 = 0; i0 < nt; i0 += 32) {
+      const int64_t i = i0 + lane;
+      int64_t n = 0;
+      if (i < nt) {
+        int lo, hi;
+        row_tile_keys<TM, KT>(s, a.G, a.window, i, lo, hi);
+        n = hi - lo;
+      }
+      int64_t v = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (i < nt) a.pre[rt + i] = (int32_t)(sum + v - n);
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) a.Wb[b + 1] = sum * a.pool.Hkv;
+  }
+  __syncthreads();
+  at = 0;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    const int64_t s = block_scan(b < B ? a.Wb[b + 1] : 0, ws, &total);
+    if (b < B) a.Wb[b + 1] = at + s;
+    at += total;
+  }
+  if (threadIdx.x == 0) a.Wb[0] = 0;
+}
+
+// ---------------------------------------------------------------- merge
+
+// Joins the pieces of the unit that begins in CTA c's part of the list and
+// ends behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
+// in that order, so the result does not depend on which CTA ran when.  One
+// warp per row, blockIdx.y picks 16 rows.
+template <typename T, int D, int TM, int KT>
+__global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
+  __shared__ int64_t wb_s[kInlineSeqs + 1];
+  const int64_t* Wb = a.Wb;
+  if (!a.planned) {
+    plan_inline<TM, KT>(a, wb_s);
+    Wb = wb_s;
+  }
+  const int64_t total = Wb[a.batch.B], share = list_share(a, total);
+  const int64_t w0 = blockIdx.x * share, w1 = w0 + share;
+  if (w1 >= total) return;
+  const Unit u = find_unit<TM, KT>(a, Wb, w1 - 1);
+  const int64_t uend = u.begin + (u.hi - u.lo);
+  if (u.begin < w0 || uend <= w1) return;
+  const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
+  const int64_t rows = (int64_t)s.n * a.G, row0 = u.i * TM;
+  const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
+  const int pieces = (int)((uend - 1) / share) - (int)blockIdx.x + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int C = D / 32;
+  auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  for (int r = blockIdx.y * 16 + warp; r < nrow && r < (int)blockIdx.y * 16 + 16; r += 8) {
+    float m = -INFINITY;
+    bool bad = false;  // NaN goes through the maximum unseen
+    for (int i = lane; i < pieces; i += 32) {
+      const float x = a.ml[slot(i) * TM + r].x;
+      m = fmaxf(m, x);
+      bad |= x != x;
+    }
+    m = warp_max(m);
+    if (__any_sync(0xffffffffu, bad)) m = NAN;
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const int64_t at = slot(i) * TM + r;
+      const float2 x = a.ml[at];
+      const float f = exp2f(x.x - ref);
+      l = fmaf(x.y, f, l);
+      const float* p = a.part + at * D + lane * C;
+#pragma unroll
+      for (int j = 0; j < C; ++j) o[j] = fmaf(p[j], f, o[j]);
+    }
+    const int64_t g = row0 + r, tok = s.r0 + g / a.G, head = u.h * a.G + g % a.G;
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    T* out = static_cast<T*>(a.out) + tok * a.ot + head * a.oh + lane * C;
+#pragma unroll
+    for (int j = 0; j < C; ++j) out[j] = Elem<T>::from_f(o[j] * inv);
+    if (lane == 0 && a.lse) a.lse[tok * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <int TM, int KT>
+cudaError_t launch_plan(const PoolAttendArgs& a, cudaStream_t st) {
+  pool_plan_kernel<TM, KT><<<1, 1024, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int TM, int KT>
+cudaError_t launch_merge(const PoolAttendArgs& a, cudaStream_t st) {
+  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas, (TM + 15) / 16), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace lod

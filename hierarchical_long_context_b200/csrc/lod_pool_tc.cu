@@ -1,0 +1,560 @@
+// lod_pool_tc.cu -- exact attention of many new tokens over the block pool on the
+// tensor cores (tcgen05, TMEM accumulators, TMA): 256 query rows per unit.
+#include "lod_pool_list.cuh"
+#include "lod_tc.cuh"
+
+namespace lod {
+namespace {
+
+constexpr int kTM = 256, kKT = 128;  // query rows of a unit, keys of a tile
+constexpr int kHalfBytes = 128 * 128;  // 128 rows x 64 bf16 channels
+
+// ---------------------------------------------------------------- PTX
+
+__device__ __forceinline__ void tma_load_box(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ uint32_t sw_off(int row, int chunk16) {  // 16-byte chunk of a 128B-swizzled row
+  return (uint32_t)(row * 128 + (((chunk16 & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// ---------------------------------------------------------------- e4m3 -> bf16
+
+// Four e4m3 codes as four bf16 (two words), each times 2^(E - 127).  Shifted
+// into a bf16's exponent and mantissa, a code's low seven bits read as the
+// code's value times 2^-120 (bias 127 against 7; a subnormal code becomes a
+// subnormal bf16), so one product by 2^120 2^(E - 127) gives the row's value
+// exactly.  f1 and f2 are that factor in two parts, as it can leave bf16's range.
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t f1, uint32_t f2, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+  const uint32_t x = ((a >> 4) & 0x07f007f0u) | (a & 0x80008000u);
+  const uint32_t y = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  lo = hmul2_bf16(hmul2_bf16(x, f1), f2);
+  hi = hmul2_bf16(hmul2_bf16(y, f1), f2);
+}
+// The two factors of exponent byte E, each in both halves of a word.
+__device__ __forceinline__ void e4m3_factors(int E, uint32_t& f1, uint32_t& f2) {
+  // 2^(120 + e) = 2^(120 + min(e, 7)) * 2^(e - min(e, 7)); E = 255: NaN.  The
+  // pool never holds e below -120; smaller ones read as 2^-120.
+  int e = E - 127;
+  e = e < -120 ? -120 : e;
+  const int e1 = e < 7 ? e : 7;
+  const uint32_t a = (uint32_t)(e1 + 120 + 127) << 7, b = E == 255 ? 0x7fc0u : (uint32_t)(e - e1 + 127) << 7;
+  f1 = a | (a << 16);
+  f2 = b | (b << 16);
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <int D, bool Q8>
+struct RowsSmem {
+  static constexpr int kTile = 128 * D * 2;  // a K, V or Q tile
+  static constexpr int kStages = D == 128 ? (Q8 ? 4 : 5) : 8;
+  static constexpr int kRaw = Q8 ? 128 * D + 128 : 0;  // codes and exponent bytes of a tile
+  static constexpr size_t off_Q = 0;                   // two query tiles
+  static constexpr size_t off_KV = off_Q + 2 * kTile;  // ring: K, V of a key tile take turns
+  static constexpr size_t off_raw = off_KV + (size_t)kStages * kTile;
+  static constexpr size_t off_bar = off_raw + 2 * kRaw;
+  static constexpr int kBars = 2 * kStages + 4 + 8 + 1;
+  static constexpr size_t off_wb = off_bar + 8 * kBars + 8;  // (only counted when the list is laid out here)
+  static constexpr size_t bytes = off_wb + 16 + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+// Roles: warp 0 TMA copies, warp 1 MMA issue (warps 2 and 3 idle); warps 4-7
+// and 8-11 the softmax of query tiles 0 and 1 (a thread per row); with an
+// 8-bit pool warps 12-15 turn codes into bf16 tiles.
+//
+// Tensor memory: S_0, S_1 (fp32, 128 columns each; the weights P_s, bf16
+// pairs, overwrite the first half of S_s), O_0, O_1.  The MMA warp issues,
+// for each key tile j and query tile s in turn, O_s += P_s V_j and
+// S_s = Q_s K_{j+1}^T; while it works on one query tile the other tile's
+// softmax runs.  MMAs of one thread run in order, so S_s(j + 1) complete
+// means O_s(j) complete: the softmax warps may then rescale O_s themselves,
+// which they do only when a row's maximum has grown by more than 2^8
+// (weights up to 2^8 are as exact as any in bf16 and fp32).
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
+    pool_rows_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
+  using S = RowsSmem<D, Q8>;
+  constexpr int NS = S::kStages;
+  constexpr int kThreads = Q8 ? 512 : 384;
+  constexpr float kTau = 8.f;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  uint64_t* empty = full + NS;
+  uint64_t* raw_full = empty + NS;
+  uint64_t* raw_empty = raw_full + 2;
+  uint64_t* s_full = raw_empty + 2;
+  uint64_t* p_ready = s_full + 2;
+  uint64_t* q_full = p_ready + 2;
+  uint64_t* o_full = q_full + 2;
+  uint64_t* fin = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], Q8 ? 4 : 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(fin, 1);
+    *abort_s = 0;
+    fence_mbar_init();
+    if (!Q8) {
+      tc::prefetch_tensormap(&maps.K);
+      tc::prefetch_tensormap(&maps.V);
+    }
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+  clear_refused<__nv_bfloat16, D>(a);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kColO = 256;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_s) return false;
+    if (mbar_wait(bar, parity, a.status)) return true;
+    *abort_s = 1;
+    return false;
+  };
+  const int shift = a.pool.shift;
+  const int per_tile = kKT >> shift;  // blocks of a key tile
+
+  if (warp < 4) {
+    regs_dec<40>();
+    if (warp == 0) {
+      // ============================================================ copies
+      Walk<kTM, kKT> w(a, a.Wb, blockIdx.x);
+      int c = 0;  // tiles copied (K and V count apart)
+      bool go = true;
+      for (; w.more() && go; w.next()) {
+        const int32_t* table = a.batch.table + (int64_t)w.u.b * a.batch.max_blocks;
+        const int nblk = (int)((w.s.len + (1 << shift) - 1) >> shift);
+        int entry = -1;  // this lane's block of the next key tile
+        auto load_entry = [&](int kt) {
+          const int i = kt * per_tile + lane;
+          entry = -1;
+          if (lane < per_tile && i < nblk && kt < w.kt1) {
+            entry = table[i];
+            if (entry < 0 || entry >= a.pool.blocks) {
+              set_status(a.status, LOD_ST_BAD_PAGE);
+              entry = -1;
+            }
+          }
+        };
+        load_entry(w.kt0);
+        for (int kt = w.kt0; kt < w.kt1 && go; ++kt) {
+          const int mine = entry;
+          load_entry(kt + 1);
+          const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
+          const int rows = __popc(ok) << shift;
+          const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++c) {
+            if constexpr (Q8) {
+              const int st = c & 1;
+              if (c >= 2 && !(go = wait(&raw_empty[st], (uint32_t)((c - 2) >> 1) & 1u))) break;
+              unsigned char* dst = sm + S::off_raw + st * S::kRaw;
+              if (lane == 0) {
+                if (rows) mbar_arrive_expect(&raw_full[st], (uint32_t)rows * (D + 1));
+                else mbar_arrive(&raw_full[st]);
+              }
+              __syncwarp();
+              if (mine >= 0) {
+                const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
+                const uint8_t* ex = kv ? a.pool.Ve : a.pool.Ke;
+                bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, &raw_full[st]);
+                bulk_g2s(dst + 128 * D + (lane << shift), ex + row, 1u << shift, &raw_full[st]);
+              }
+            } else {
+              const int st = c % NS;
+              if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
+              unsigned char* dst = sm + S::off_KV + (size_t)st * S::kTile;
+              if (lane == 0) {
+                if (rows) mbar_arrive_expect(&full[st], (uint32_t)rows * D * 2);
+                else mbar_arrive(&full[st]);
+              }
+              __syncwarp();
+              if (mine >= 0) {
+                const CUtensorMap* map = kv ? &maps.V : &maps.K;
+                unsigned char* d = dst + (lane << shift) * 128;
+                tma_load_box(d, map, 0, (int)row, &full[st]);
+                if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, &full[st]);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (*abort_s && lane == 0) {  // copies still in flight land before the CTA ends
+        const int n = Q8 ? 2 : NS;
+        for (int i = c - 1; i >= 0 && i >= c - n; --i)
+          (void)mbar_wait(Q8 ? &raw_full[i % n] : &full[i % n], (uint32_t)(i / n) & 1u, a.status);
+      }
+    } else if (warp == 1) {
+      // ============================================================ MMA issue
+      if (lane == 0) {
+        const uint32_t idS = tc::idesc_bf16(128, 128, false, false);
+        const uint32_t idO = tc::idesc_bf16(128, D, false, true);
+        const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
+        Walk<kTM, kKT> w(a, a.Wb, blockIdx.x);
+        int c = 0;                          // ring position of the next K tile (V follows it)
+        uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // weights and query tiles taken
+        bool go = true, any = false;
+        auto full_wait = [&](int x) { return wait(&full[x % NS], (uint32_t)(x / NS) & 1u); };
+        auto scores = [&](int s, int x) {  // S_s = Q_s K^T, K at ring position x
+          const uint32_t qs = qb + s * S::kTile, ks = kvb + (uint32_t)(x % NS) * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
+            tc::mma_bf16(tmem + s * 128, tc::desc_kmajor_sw128(qs + o), tc::desc_kmajor_sw128(ks + o), idS, kk > 0);
+          }
+          tc::mma_commit(&s_full[s]);
+          any = true;
+        };
+        for (; w.more() && go; w.next()) {
+          const int tiles = w.nrow > 128 ? 2 : 1;
+          const int T = w.kt1 - w.kt0;
+          for (int s = 0; s < tiles && go; ++s) go = wait(&q_full[s], nq[s]++ & 1u);
+          if (!go || !(go = full_wait(c))) break;
+          tc::fence_after_sync();
+          for (int s = 0; s < tiles; ++s) scores(s, c);
+          tc::mma_commit(&empty[c % NS]);
+          for (int j = 0; j < T && go; ++j, c += 2) {
+            for (int s = 0; s < tiles; ++s) {
+              if (!(go = wait(&p_ready[s], np[s]++ & 1u))) break;
+              if (s == 0 && !(go = full_wait(c + 1))) break;
+              tc::fence_after_sync();
+              const uint32_t vs = kvb + (uint32_t)((c + 1) % NS) * S::kTile;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc::mma_bf16_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * kk,
+                                tc::desc_mnmajor_sw128(vs + kk * 2048, kHalfBytes), idO, j > 0 || kk > 0);
+              if (s == tiles - 1) tc::mma_commit(&empty[(c + 1) % NS]);
+              if (j + 1 < T) {
+                if (s == 0 && !(go = full_wait(c + 2))) break;
+                tc::fence_after_sync();
+                scores(s, c + 2);
+                if (s == tiles - 1) tc::mma_commit(&empty[(c + 2) % NS]);
+              } else {
+                tc::mma_commit(&o_full[s]);
+              }
+            }
+          }
+        }
+        if (any) {
+          tc::mma_commit(fin);
+          (void)mbar_wait(fin, 0, a.status);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    // ============================================================== softmax
+    regs_inc<Q8 ? 200 : 232>();
+    const int s = (warp - 4) >> 2;  // query tile
+    const int r = tid & 127;
+    const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + tl + s * 128, to = tmem + tl + kColO + s * 128;
+    const float scl = a.scale_log2;
+    unsigned char* Qs = sm + S::off_Q + s * S::kTile;
+    uint32_t ns = 0, no = 0;  // scores and outputs taken
+    int c = 0;                // ring position of the next key tile's K
+    bool go = true;
+    for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+      const int T = w.kt1 - w.kt0;
+      if (s * 128 >= w.nrow) {
+        c += 2 * T;
+        continue;
+      }
+      const int G = a.G, last = min(w.nrow - 1 - s * 128, 127);
+      const bool mine = r <= last;
+      const int g = (int)w.u.i * kTM + s * 128 + (mine ? r : last);  // (a row past the end does as the last one)
+      const int tok = g / G, head = w.u.h * G + g % G;
+      const int p0 = (int)(w.s.len - w.s.n);
+      const int pos = p0 + tok;
+      {
+        const __nv_bfloat16* src =
+            static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + tok) * a.qt + (int64_t)head * a.qh;
+        uint4 x[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = mine ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(Qs + (i >> 3) * kHalfBytes + sw_off(r, i)) = x[i];
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[s]);
+      }
+      // positions of the tile's first and last row; a bad block anywhere in
+      // the piece sends its tiles through the masks
+      const int pos_lo = p0 + ((int)w.u.i * kTM + s * 128) / G, pos_hi = p0 + ((int)w.u.i * kTM + s * 128 + last) / G;
+      const int32_t* table = a.batch.table + (int64_t)w.u.b * a.batch.max_blocks;
+      const int nblk = (int)((w.s.len + (1 << shift) - 1) >> shift);
+      bool bad = false;
+      for (int i = w.kt0 * per_tile + r; i < nblk && i < w.kt1 * per_tile; i += 128)
+        bad |= table[i] < 0 || table[i] >= a.pool.blocks;
+      const bool unit_bad = bar_red_or(1 + s, 128, bad);
+      const int first = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;  // this row's keys
+      const int first_hi = a.window > 0 && pos_hi - a.window + 1 > 0 ? (int)(pos_hi - a.window + 1) : 0;
+
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < T; ++j, c += 2) {
+        const int k0 = (w.kt0 + j) * kKT;
+        const bool masked = k0 + 127 > pos_lo || k0 < first_hi || unit_bad;
+        const bool ragged = k0 + 127 >= w.s.len || unit_bad;  // V rows that are no keys
+        go = __all_sync(0xffffffffu, wait(&s_full[s], ns++ & 1u));
+        if (!go) break;
+        tc::fence_after_sync();
+        float y[128];
+        tc::tmem_ld32xN<4>(ts, y);
+        if (masked) {
+          const int hi = pos - k0, lo = first - k0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) y[e] = e <= hi && e >= lo ? y[e] : -INFINITY;
+          if (unit_bad) {
+            for (int x = 0; x < per_tile; ++x) {
+              const int i = (w.kt0 + j) * per_tile + x;
+              if (i < nblk && table[i] >= 0 && table[i] < a.pool.blocks) continue;
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                if (e >> shift == x) y[e] = -INFINITY;
+            }
+          }
+        }
+        if (ragged) {
+          // P's zeros must not meet what the pool holds behind the length or
+          // what shared memory held before: those V rows become zero
+          go = __all_sync(0xffffffffu, wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u));
+          if (!go) break;
+          const int t = k0 + r, i = t >> shift;
+          if (t >= w.s.len || table[i] < 0 || table[i] >= a.pool.blocks) {
+            unsigned char* v = sm + S::off_KV + (size_t)((c + 1) % NS) * S::kTile;
+#pragma unroll
+            for (int q = 0; q < D / 8; ++q)
+              *reinterpret_cast<uint4*>(v + (q >> 3) * kHalfBytes + sw_off(r, q)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+        }
+        float mx[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+        for (int e = 4; e < 124; e += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], y[e + q], y[e + 4 + q]);
+        }
+        float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        top = fmaxf(max3(top, y[124], y[125]), fmaxf(y[126], y[127])) * scl;
+        const bool need = top > m + kTau || j == 0;
+        if (__any_sync(0xffffffffu, need)) {
+          const float mn = need ? fmaxf(top, m) : m;
+          const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+          m = mn;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              float o[32];
+              tc::tmem_ld32(to + 32 * q, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tc::tmem_st32(to + 32 * q, o);
+            }
+          }
+        }
+        const float2 sc2 = make_float2(scl, scl);
+        const float mu = m == -INFINITY ? 0.f : m;
+        const float2 mu2 = make_float2(-mu, -mu);
+        float2 la[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) la[q] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
+            t.x = ex2_approx(t.x);
+            t.y = ex2_approx(t.y);
+            la[e & 3] = fadd2(la[e & 3], t);
+            pw[e] = pack_bf16x2(t.x, t.y);
+          }
+          tmem_st16(ts + 16 * q, pw);
+        }
+        tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[s]);
+        const float2 l2 = fadd2(fadd2(la[0], la[1]), fadd2(la[2], la[3]));
+        l += l2.x + l2.y;
+      }
+      if (!go) break;
+      // ---- the rows' results
+      go = __all_sync(0xffffffffu, wait(&o_full[s], no++ & 1u));
+      if (!go) break;
+      tc::fence_after_sync();
+      const bool whole = w.whole();
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const int64_t at = (int64_t)w.slot(blockIdx.x) * kTM + s * 128 + r;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tc::tmem_ld32(to + 32 * q, o);
+        if (mine && whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4*>(out)[4 * q + e] =
+                make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                           pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                           pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+        } else if (mine) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<float4*>(a.part + at * D)[8 * q + e] =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        __syncwarp();
+      }
+      if (mine) {
+        if (!whole) a.ml[at] = make_float2(m, l);
+        else if (a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
+      }
+      tc::fence_before_sync();  // O_s is read before the next unit's weights are announced
+    }
+  } else if constexpr (Q8) {
+    // ============================================================== codes to bf16 tiles
+    regs_dec<72>();
+    int c = 0;
+    bool go = true;
+    constexpr int CPR = D / 16;  // 16-code chunks of a row
+    for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+      for (int x = 0; x < 2 * (w.kt1 - w.kt0); ++x, ++c) {
+        go = __all_sync(0xffffffffu, wait(&raw_full[c & 1], (uint32_t)(c >> 1) & 1u) &&
+                                         (c < NS || wait(&empty[c % NS], (uint32_t)(c / NS - 1) & 1u)));
+        if (!go) break;
+        const unsigned char* src = sm + S::off_raw + (c & 1) * S::kRaw;
+        unsigned char* dst = sm + S::off_KV + (size_t)(c % NS) * S::kTile;
+        const int t = tid & 127;
+#pragma unroll 2
+        for (int i = t; i < 128 * CPR; i += 128) {
+          const int row = i / CPR, ch = i % CPR;
+          const uint4 v = *reinterpret_cast<const uint4*>(src + i * 16);
+          uint32_t f1, f2;
+          e4m3_factors(src[128 * D + row], f1, f2);
+          uint4 o0, o1;
+          e4m3x4_bf16(v.x, f1, f2, o0.x, o0.y);
+          e4m3x4_bf16(v.y, f1, f2, o0.z, o0.w);
+          e4m3x4_bf16(v.z, f1, f2, o1.x, o1.y);
+          e4m3x4_bf16(v.w, f1, f2, o1.z, o1.w);
+          // a row's two halves lie on the same banks: the lanes of the second
+          // half store their two chunks in the other order
+          const bool swap = D == 128 && (ch & 4);
+          const int c0 = 2 * ch + (swap ? 1 : 0), c1 = 2 * ch + (swap ? 0 : 1);
+          unsigned char* d = dst + (ch >> 2) * kHalfBytes;
+          *reinterpret_cast<uint4*>(d + sw_off(row, c0)) = swap ? o1 : o0;
+          *reinterpret_cast<uint4*>(d + sw_off(row, c1)) = swap ? o0 : o1;
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[c & 1]);
+          mbar_arrive(&full[c % NS]);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// The register split (setmaxnreg) draws on what the CTA was launched with: a
+// build whose kernel has fewer registers a thread would wait for ever, so it
+// is refused instead.  Checked once per kernel.
+template <auto Kern>
+cudaError_t check_registers(int needed) {
+  static std::atomic<int> have{-1};
+  int n = have.load(std::memory_order_relaxed);
+  if (n < 0) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, Kern);
+    if (e != cudaSuccess) return e;
+    have.store(n = at.numRegs, std::memory_order_relaxed);
+  }
+  return n >= needed ? cudaSuccess : cudaErrorLaunchOutOfResources;
+}
+
+template <int D, bool Q8>
+cudaError_t launch_rows(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
+  cudaError_t e = set_smem_once<pool_rows_kernel<D, Q8>>(RowsSmem<D, Q8>::bytes);
+  // 128 (40 + 232 + 232) = 384 * 168 and 128 (40 + 200 + 200 + 72) = 512 * 128
+  if (e == cudaSuccess) e = check_registers<pool_rows_kernel<D, Q8>>(Q8 ? 128 : 168);
+  if (e == cudaSuccess) e = launch_plan<kTM, kKT>(a, st);
+  if (e != cudaSuccess) return e;
+  PoolMaps none = {};
+  pool_rows_kernel<D, Q8><<<a.ctas, Q8 ? 512 : 384, RowsSmem<D, Q8>::bytes, st>>>(maps ? *maps : none, a);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, kTM, kKT>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_pool_rows(const PoolAttendArgs& a, const PoolMaps* maps, int bits, int d, cudaStream_t stream) {
+  if (d == 64) return bits == 8 ? launch_rows<64, true>(a, maps, stream) : launch_rows<64, false>(a, maps, stream);
+  return bits == 8 ? launch_rows<128, true>(a, maps, stream) : launch_rows<128, false>(a, maps, stream);
+}
+
+}  // namespace lod

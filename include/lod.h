@@ -411,7 +411,7 @@ int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q
  * infinity or NaN is stored with E = 255 and reads NaN in every channel.
  * Supported: dtype F32 or BF16, bits 0 or 8, d in {64, 128}, block in
  * {16, 32, 64, 128}, Hq a multiple of Hkv with Hq/Hkv <= 64, blocks * Hkv *
- * block < 2^31.  K and V are 16-byte aligned device memory.
+ * block < 2^31.  K, V, Ke and Ve are 16-byte aligned device memory.
  */
 typedef struct lod_pool {
   int32_t dtype; /* lod_dtype: q, k, v and out, and the rows with bits = 0 */
