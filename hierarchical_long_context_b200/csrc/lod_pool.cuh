@@ -284,7 +284,7 @@ cudaError_t launch_pool_read(const ReadArgs& a, int dtype, int bits, int d, cuda
 
 // Shape of an attention call: which kernel, its tiles and its CTAs.
 struct PoolShape {
-  int kind;  // 0: CUDA cores; 1: tensor cores, 256 rows a unit
+  int kind;  // 0: CUDA cores (fp32); 1: tensor cores, 256 rows a unit; 2: tensor cores, few rows
   int TM, KT, ctas;
   bool inline_plan;
   size_t off_plan, off_ml, off_part, total;  // workspace offsets
@@ -296,6 +296,8 @@ struct __align__(64) PoolMaps {
 };
 // Tensor cores, many rows: bf16 rows or e4m3 codes.
 cudaError_t launch_pool_rows(const PoolAttendArgs& a, const PoolMaps* maps, int bits, int d, cudaStream_t stream);
+// Tensor cores, at most TM = 8, 16, 32 or 64 rows per sequence and KV head.
+cudaError_t launch_pool_few(const PoolAttendArgs& a, const PoolMaps* maps, int TM, int bits, int d, cudaStream_t stream);
 
 cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, const PoolMaps* maps, int dtype, int bits, int d,
                                cudaStream_t stream);

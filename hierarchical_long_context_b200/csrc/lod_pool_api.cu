@@ -304,7 +304,7 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
   a.ctas = s.ctas;
   a.min_share = 1;
   lod::PoolMaps maps;
-  const bool tma = s.kind == 1 && pool->bits == 0;
+  const bool tma = s.kind != 0 && pool->bits == 0;
   if (tma) {
     const cuuint64_t dims[2] = {(cuuint64_t)pool->d, (cuuint64_t)(pool->blocks * pool->Hkv * pool->block)};
     const cuuint64_t row[1] = {(cuuint64_t)pool->d * 2};

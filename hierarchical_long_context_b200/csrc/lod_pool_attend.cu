@@ -248,8 +248,14 @@ cudaError_t launch_simt_d(const PoolAttendArgs& a, int TM, int bits, cudaStream_
 
 PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms) {
   PoolShape s = {};
-  s.kind = dtype == LOD_DTYPE_BF16 && max_new * G > 64 ? 1 : 0;
-  if (s.kind == 1) {
+  const int64_t rows = max_new * G;
+  s.kind = dtype != LOD_DTYPE_BF16 ? 0 : rows > 64 ? 1 : 2;
+  if (s.kind == 2) {
+    s.TM = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    s.KT = 128;
+    s.ctas = sms;
+    s.inline_plan = B <= kInlineSeqs;
+  } else if (s.kind == 1) {
     s.TM = 256;
     s.KT = 128;
     s.ctas = sms;
@@ -273,10 +279,8 @@ PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_
 cudaError_t launch_pool_attend(PoolAttendArgs& a, const PoolShape& s, const PoolMaps* maps, int dtype, int bits, int d,
                                cudaStream_t stream) {
   if (s.kind == 1) return launch_pool_rows(a, maps, bits, d, stream);
-  if (dtype == LOD_DTYPE_F32)
-    return d == 64 ? launch_simt_d<float, 64>(a, s.TM, bits, stream) : launch_simt_d<float, 128>(a, s.TM, bits, stream);
-  return d == 64 ? launch_simt_d<__nv_bfloat16, 64>(a, s.TM, bits, stream)
-                 : launch_simt_d<__nv_bfloat16, 128>(a, s.TM, bits, stream);
+  if (s.kind == 2) return launch_pool_few(a, maps, s.TM, bits, d, stream);
+  return d == 64 ? launch_simt_d<float, 64>(a, s.TM, bits, stream) : launch_simt_d<float, 128>(a, s.TM, bits, stream);
 }
 
 }  // namespace lod

@@ -1,0 +1,545 @@
+// lod_pool_few.cu -- exact attention of few new tokens (at most 64 query rows per
+// sequence and KV head) over the block pool: the cache streams past once.
+#include "lod_pool_list.cuh"
+#include "lod_pool_tc.cuh"
+
+namespace lod {
+namespace {
+
+template <int D, int RQ, bool Q8>
+struct FewSmem {
+  static constexpr int NQ = RQ < 16 ? 16 : RQ;  // the MMAs' N (a multiple of 16 with M = 128)
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kWide = D == 64 ? 2 : 1;  // d = 64 has room for twice the stages
+  // stages: what 227 KB hold beside the query and weight tiles
+  static constexpr int KS = kWide * (Q8 ? 1 : RQ == 64 ? 2 : 3);
+  static constexpr int VS = kWide * (Q8 ? (RQ == 64 ? 1 : 2) : RQ >= 32 ? 2 : 3);
+  static constexpr int RS = kWide * (RQ >= 32 ? 2 : 3);  // stages of codes (K and V of a tile)
+  static constexpr int kRaw = 128 * D + 128;
+  static constexpr int kQ = NQ * D * 2, kP = NQ * 256;
+  static constexpr size_t off_V = 0;  // (with d = 64 MMA 2 reads one tile past a V tile: K tiles follow)
+  static constexpr size_t off_K = off_V + (size_t)VS * kTile;
+  static constexpr size_t off_P = off_K + (size_t)KS * kTile;  // [2][2 key halves][NQ][128 B]
+  static constexpr size_t off_Q = off_P + 2 * kP;              // [2][D / 64 halves][NQ][128 B]
+  static constexpr size_t off_raw = off_Q + 2 * kQ;
+  static constexpr size_t off_ex = off_raw + (Q8 ? (size_t)RS * 2 * kRaw : 0);  // uint8 [4][2][128]
+  static constexpr size_t off_m = off_ex + (Q8 ? 1024 : 0);                     // float [NQ]
+  static constexpr size_t off_red = off_m + 4 * 64;                             // float [4][64]
+  static constexpr size_t off_pos = off_red + 4 * 4 * 64;                       // int2 [64]
+  static constexpr size_t off_info = off_pos + 8 * 64;                          // uint32 [16]
+  static constexpr size_t off_wb = off_info + 64;                               // int64 [kInlineSeqs + 1]
+  static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 1;
+  static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
+  static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+  // exponent bytes are kept for 4 tiles: the codes' warps run at most KS + 2
+  // (K) and VS (V) tiles ahead of the softmax; block masks for 16: the copies
+  // run at most RS tiles ahead of those (8-bit), or KS, VS ahead
+  static_assert(!Q8 || (KS <= 2 && VS <= 4), "exponent ring");
+  static_assert(RS + VS + 2 <= 16, "block mask ring");
+};
+
+// The cache is the A operand: S^T = K Q^T (M = 128 keys, N = query rows), so
+// a thread of the softmax owns a key, an 8-bit row's exponent is one factor
+// of that thread, and few query rows cost few columns rather than a padded
+// tile of 128 rows; O^T += V^T P^T (M = channels).  A tile's weights are
+// taken against a reference maximum per query row; only when some score
+// exceeds it by more than 2^8 (and on a unit's first tile) does the
+// warpgroup find new maxima and rescale O^T.
+// Roles: warp 0 TMA copies, warp 1 MMA issue, warps 2 and 3 query tiles,
+// warps 4-7 softmax, with an 8-bit pool warps 8-11 codes to bf16.
+// Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
+// HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
+template <int D, int RQ, bool Q8>
+__global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
+    pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
+  using S = FewSmem<D, RQ, Q8>;
+  constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
+  constexpr float kTau = 8.f;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + S::off_bar);
+  uint64_t* kempty = kfull + KS;
+  uint64_t* vfull = kempty + KS;
+  uint64_t* vempty = vfull + VS;
+  uint64_t* raw_full = vempty + VS;       // [RS][2]
+  uint64_t* raw_empty = raw_full + 2 * RS;
+  uint64_t* s_full = raw_empty + 2 * RS;  // [2]
+  uint64_t* s_free = s_full + 2;
+  uint64_t* p_ready = s_free + 2;
+  uint64_t* pv_done = p_ready + 2;
+  uint64_t* q_full = pv_done + 2;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* fin = q_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* m_s = reinterpret_cast<float*>(sm + S::off_m);
+  float* red_s = reinterpret_cast<float*>(sm + S::off_red);
+  int2* pos_s = reinterpret_cast<int2*>(sm + S::off_pos);
+  volatile uint32_t* info_s = reinterpret_cast<volatile uint32_t*>(sm + S::off_info);
+  unsigned char* ex_s = sm + S::off_ex;
+  int64_t* wb_s = reinterpret_cast<int64_t*>(sm + S::off_wb);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 32) {
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(&kfull[i], Q8 ? 4 : 1);
+      mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(&vfull[i], Q8 ? 4 : 1);
+      mbar_init(&vempty[i], 1);
+    }
+    for (int i = 0; i < 2 * RS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+      mbar_init(&p_ready[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 2);
+      mbar_init(&q_empty[i], 1);
+    }
+    mbar_init(fin, 1);
+    *abort_s = 0;
+    fence_mbar_init();
+    if (!Q8) {
+      tc::prefetch_tensormap(&maps.K);
+      tc::prefetch_tensormap(&maps.V);
+    }
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 256);
+  for (int i = tid; i < 2 * S::kP / 16; i += blockDim.x)  // rows of P past RQ stay zero
+    reinterpret_cast<uint4*>(sm + S::off_P)[i] = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async();
+  const int64_t* Wb = a.Wb;
+  if (!a.planned) {
+    plan_inline<RQ, kKT>(a, wb_s);
+    Wb = wb_s;
+  }
+  clear_refused<__nv_bfloat16, D>(a);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kColO = 128;  // S^T in columns [0, 64) and [64, 128)
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (*abort_s) return false;
+    if (mbar_wait(bar, parity, a.status)) return true;
+    *abort_s = 1;
+    return false;
+  };
+  // wait for use number `i` of a ring of n barriers
+  auto wait_ring = [&](uint64_t* bars, int n, int i) { return wait(&bars[i % n], (uint32_t)(i / n) & 1u); };
+  const int shift = a.pool.shift;
+  const int per_tile = kKT >> shift;
+  const uint32_t all_ok = (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1);
+
+  if (warp == 0) {
+    // ============================================================== copies
+    int c = 0;  // key tiles
+    bool go = true;
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
+      const int32_t* table = a.batch.table + (int64_t)w.u.b * a.batch.max_blocks;
+      const int nblk = (int)((w.s.len + (1 << shift) - 1) >> shift);
+      int entry = -1;  // this lane's block of the next key tile
+      auto load_entry = [&](int kt) {
+        const int i = kt * per_tile + lane;
+        entry = -1;
+        if (lane < per_tile && i < nblk && kt < w.kt1) {
+          entry = table[i];
+          if (entry < 0 || entry >= a.pool.blocks) {
+            set_status(a.status, LOD_ST_BAD_PAGE);
+            entry = -1;
+          }
+        }
+      };
+      load_entry(w.kt0);
+      for (int kt = w.kt0; kt < w.kt1 && go; ++kt, ++c) {
+        const int mine = entry;
+        load_entry(kt + 1);
+        const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
+        const int rows = __popc(ok) << shift;
+        const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
+        if (!Q8 && lane == 0) info_s[c & 15] = ok;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if constexpr (Q8) {
+            uint64_t* bar = &raw_full[(c % RS) * 2 + kv];
+            if (c >= RS && !(go = wait(&raw_empty[(c % RS) * 2 + kv], (uint32_t)(c / RS - 1) & 1u))) break;
+            unsigned char* dst = sm + S::off_raw + ((c % RS) * 2 + kv) * S::kRaw;
+            if (lane == 0) {
+              if (kv == 0) info_s[c & 15] = ok;
+              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * (D + 1));
+              else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (mine >= 0) {
+              const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
+              const uint8_t* ex = kv ? a.pool.Ve : a.pool.Ke;
+              bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, bar);
+              bulk_g2s(dst + 128 * D + (lane << shift), ex + row, 1u << shift, bar);
+            }
+          } else {
+            const int n = kv ? VS : KS, st = c % n;
+            uint64_t* bar = (kv ? vfull : kfull) + st;
+            if (c >= n && !(go = wait((kv ? vempty : kempty) + st, (uint32_t)(c / n - 1) & 1u))) break;
+            unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)st * S::kTile;
+            if (lane == 0) {
+              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * D * 2);
+              else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (mine >= 0) {
+              const CUtensorMap* map = kv ? &maps.V : &maps.K;
+              unsigned char* d = dst + (lane << shift) * 128;
+              tma_load_box(d, map, 0, (int)row, bar);
+              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, bar);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (*abort_s && lane == 0) {  // copies still in flight land before the CTA ends
+      for (int kv = 0; kv < 2; ++kv) {
+        const int n = Q8 ? RS : kv ? VS : KS;
+        // (the last tile's copies may not have been issued: its barrier then
+        // times out once and the CTA ends)
+        for (int i = c - 1; i >= 0 && i >= c - n; --i)
+          (void)mbar_wait(Q8 ? &raw_full[(i % n) * 2 + kv] : (kv ? vfull : kfull) + i % n, (uint32_t)(i / n) & 1u,
+                          a.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ============================================================== MMA issue
+    if (lane == 0) {
+      const uint32_t idS = tc::idesc_bf16(128, NQ, false, false);
+      const uint32_t idO = tc::idesc_bf16(128, NQ, true, false);
+      const uint32_t qb = smem_u32(sm + S::off_Q), pb = smem_u32(sm + S::off_P);
+      const uint32_t kb = smem_u32(sm + S::off_K), vb = smem_u32(sm + S::off_V);
+      int c = 0, k = 0;  // key tiles, units
+      bool go = true, any = false;
+      auto values = [&](int x, bool acc) -> bool {  // O^T (+)= V_x^T P_x^T
+        if (!wait_ring(p_ready, 2, x) || !wait_ring(vfull, VS, x)) return false;
+        tc::fence_after_sync();
+        const uint32_t vs = vb + (uint32_t)(x % VS) * S::kTile, ps = pb + (uint32_t)(x & 1) * S::kP;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16(tmem + kColO, tc::desc_mnmajor_sw128(vs + kk * 2048, kHalfBytes),
+                       tc::desc_kmajor_sw128(ps + (kk >> 2) * NQ * 128 + (kk & 3) * 32), idO, acc || kk > 0);
+        tc::mma_commit(&vempty[x % VS]);
+        tc::mma_commit(&pv_done[x & 1]);
+        return true;
+      };
+      for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
+        if (!(go = wait_ring(q_full, 2, k))) break;
+        const uint32_t qs = qb + (uint32_t)(k & 1) * S::kQ;
+        const int T = w.kt1 - w.kt0;
+        for (int j = 0; j < T && go; ++j, ++c) {
+          if (!(go = wait_ring(kfull, KS, c))) break;
+          if (c >= 2 && !(go = wait_ring(s_free, 2, c - 2))) break;
+          tc::fence_after_sync();
+          const uint32_t ks = kb + (uint32_t)(c % KS) * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_bf16(tmem + (c & 1) * 64, tc::desc_kmajor_sw128(ks + (kk >> 2) * kHalfBytes + (kk & 3) * 32),
+                         tc::desc_kmajor_sw128(qs + (kk >> 2) * NQ * 128 + (kk & 3) * 32), idS, kk > 0);
+          tc::mma_commit(&kempty[c % KS]);
+          tc::mma_commit(&s_full[c & 1]);
+          if (j == T - 1) tc::mma_commit(&q_empty[k & 1]);
+          any = true;
+          if (j > 0) go = values(c - 1, j > 1);
+          if (go && j == T - 1) go = values(c, j > 0);
+        }
+      }
+      if (any) {
+        tc::mma_commit(fin);
+        (void)mbar_wait(fin, 0, a.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ============================================================== query tiles
+    int k = 0;
+    bool go = true;
+    const int r0 = tid - 64;
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
+      if (k >= 2 && !(go = __all_sync(0xffffffffu, wait_ring(q_empty, 2, k - 2)))) break;
+      unsigned char* qs = sm + S::off_Q + (size_t)(k & 1) * S::kQ;
+      for (int x = r0; x < NQ * (D / 8); x += 64) {
+        const int r = x / (D / 8), ch = x % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < w.nrow) {
+          const int g = (int)w.u.i * RQ + r;
+          v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + g / a.G) * a.qt +
+                                              (int64_t)(w.u.h * a.G + g % a.G) * a.qh + ch * 8);
+        }
+        *reinterpret_cast<uint4*>(qs + (ch >> 3) * NQ * 128 + sw_off(r, ch)) = v;
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[k & 1]);
+    }
+  } else if (warp < 8) {
+    // ============================================================== softmax
+    const int r = tid & 127;  // key of the tile; channel of O^T
+    const int q4 = warp & 3;
+    const uint32_t tl = (uint32_t)(32 * q4) << 16;
+    constexpr int CH = RQ < 16 ? 8 : 16;  // columns of a TMEM load
+    auto load_cols = [&](uint32_t at, float (&v)[CH]) {
+      if constexpr (CH == 8) tc::tmem_ld8(at, v);
+      else tc::tmem_ld16(at, v);
+    };
+    int c = 0;
+    bool go = true;
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
+      const int T = w.kt1 - w.kt0;
+      const int p0 = (int)(w.s.len - w.s.n), g0 = (int)w.u.i * RQ;
+      const int pos_lo = p0 + g0 / a.G, pos_hi = p0 + (g0 + w.nrow - 1) / a.G;
+      auto first_of = [&](int pos) { return a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0; };
+      const int first_lo = first_of(pos_lo), first_hi = first_of(pos_hi);
+      bar_named_sync(2, 128);  // the last unit's readers are done
+      if (r < RQ) {
+        const int pos = p0 + (g0 + (r < w.nrow ? r : w.nrow - 1)) / a.G;
+        pos_s[r] = make_int2(first_of(pos), pos);  // the row's keys
+        m_s[r] = -INFINITY;
+      }
+      bar_named_sync(2, 128);
+      float l[RQ];
+#pragma unroll
+      for (int n = 0; n < RQ; ++n) l[n] = 0.f;
+      for (int j = 0; j < T; ++j, ++c) {
+        const int k0 = (w.kt0 + j) * kKT, t = k0 + r;
+        go = __all_sync(0xffffffffu, wait_ring(s_full, 2, c) && wait_ring(vfull, VS, c));
+        // (a failed wait is carried to the barrier below, where the four warps leave together)
+        const uint32_t ok = info_s[c & 15];
+        const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
+        const bool live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
+        float ks = a.scale_log2, vs = 1.f;
+        if constexpr (Q8) {
+          const int e0 = ex_s[(c & 3) * 256 + r], e1 = ex_s[(c & 3) * 256 + 128 + r];
+          ks *= e0 == 255 ? NAN : __uint_as_float((uint32_t)max(e0, 7) << 23);
+          vs = e1 == 255 ? NAN : __uint_as_float((uint32_t)max(e1, 7) << 23);
+        } else if (masked && go && (!live || t < first_lo)) {
+          // no row's key: the weights' zeros must not meet what the pool
+          // holds there, or what shared memory held before
+          unsigned char* v = sm + S::off_V + (size_t)(c % VS) * S::kTile;
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q)
+            *reinterpret_cast<uint4*>(v + (q >> 3) * kHalfBytes + sw_off(r, q)) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+        tc::fence_after_sync();
+        float y[RQ];
+        const uint32_t st = tmem + tl + (c & 1) * 64;
+#pragma unroll
+        for (int n0 = 0; n0 < RQ; n0 += CH) {
+          float v[CH];
+          load_cols(st + n0, v);
+#pragma unroll
+          for (int n = 0; n < CH; ++n) y[n0 + n] = v[n] * ks;
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[c & 1]);
+        if (masked) {
+#pragma unroll
+          for (int n = 0; n < RQ; ++n) {
+            const int2 fl = pos_s[n];
+            y[n] = live && t >= fl.x && t <= fl.y ? y[n] : -INFINITY;
+          }
+        }
+        bool grow = j == 0 || !go;
+#pragma unroll
+        for (int n = 0; n < RQ; n += 4) {
+          const float4 mr = *reinterpret_cast<const float4*>(m_s + n);
+          grow |= y[n] > mr.x + kTau || y[n + 1] > mr.y + kTau || y[n + 2] > mr.z + kTau || y[n + 3] > mr.w + kTau;
+        }
+        if (bar_red_or(1, 128, grow)) {
+          go = !bar_red_or(1, 128, !go);
+          if (!go) break;
+          // new maxima: over the warp's keys, then over the four warps
+#pragma unroll
+          for (int n = 0; n < RQ; ++n) {
+            const float x = warp_max(y[n]);
+            if (lane == n % 32) red_s[q4 * 64 + n] = x;
+          }
+          bar_named_sync(2, 128);
+          float f[RQ];
+#pragma unroll
+          for (int n = 0; n < RQ; ++n) {
+            const float x = fmaxf(fmaxf(red_s[n], red_s[64 + n]), fmaxf(red_s[128 + n], red_s[192 + n]));
+            const float m = m_s[n];
+            f[n] = x > m ? (m == -INFINITY ? 0.f : ex2_approx(m - x)) : 1.f;
+            l[n] *= f[n];
+          }
+          if (j > 0) {
+            go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 1));
+            if (go) {
+              tc::fence_after_sync();
+#pragma unroll
+              for (int n0 = 0; n0 < RQ; n0 += 8) {
+                float o[8];
+                tc::tmem_ld8(tmem + tl + kColO + n0, o);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) o[n] *= f[n0 + n];
+                tc::tmem_st8(tmem + tl + kColO + n0, o);
+              }
+            }
+          }
+          bar_named_sync(2, 128);  // every thread has read m_s
+          if (r < RQ) {
+            const float x = fmaxf(fmaxf(red_s[r], red_s[64 + r]), fmaxf(red_s[128 + r], red_s[192 + r]));
+            m_s[r] = fmaxf(x, m_s[r]);
+          }
+          if (bar_red_or(1, 128, !go)) {
+            go = false;
+            break;
+          }
+        }
+        // weights
+        if (c >= 2) go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 2));
+        unsigned char* P = sm + S::off_P + (size_t)(c & 1) * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
+        const int ch = (r & 63) >> 3;
+#pragma unroll
+        for (int n = 0; n < RQ; n += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(m_s + n);
+          const float mr[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]));
+            l[n + q] += p;
+            const float x = Q8 ? (masked && y[n + q] == -INFINITY ? 0.f : p * vs) : p;
+            *reinterpret_cast<__nv_bfloat16*>(P + (n + q) * 128 + ((ch ^ ((n + q) & 7)) << 4)) = __float2bfloat16_rn(x);
+          }
+        }
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[c & 1]);
+      }
+      if (!go) break;
+      // ---- the unit's result, or this CTA's piece of it
+      go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 1));
+      tc::fence_after_sync();
+#pragma unroll
+      for (int n = 0; n < RQ; ++n) {
+        const float x = warp_sum(l[n]);
+        if (lane == n % 32) red_s[q4 * 64 + n] = x;
+      }
+      if (bar_red_or(1, 128, !go)) {
+        go = false;
+        break;
+      }
+      const bool whole = w.whole();
+      const int64_t at = (int64_t)w.slot(blockIdx.x) * RQ;
+#pragma unroll 1
+      for (int n0 = 0; n0 < RQ; n0 += 8) {
+        float o[8];
+        tc::tmem_ld8(tmem + tl + kColO + n0, o);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int row = n0 + n;
+          if (row < w.nrow) {
+            const float sum = (red_s[row] + red_s[64 + row]) + (red_s[128 + row] + red_s[192 + row]);
+            const int g = g0 + row, tok = g / a.G, head = w.u.h * a.G + g % a.G;
+            if (whole) {
+              const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+              if (r < D)
+                (static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh)[r] =
+                    __float2bfloat16_rn(o[n] * inv);
+              if (r == 0 && a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m_s[row] + log2f(sum)) * 0.6931471805599453f;
+            } else {
+              if (r < D) a.part[(at + row) * D + r] = o[n];
+              if (r == 0) a.ml[at + row] = make_float2(m_s[row], sum);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before_sync();
+    }
+  } else if constexpr (Q8) {
+    // ============================================================== codes to bf16 tiles
+    int c = 0;
+    bool go = true;
+    constexpr int CPR = D / 16;  // 16-code chunks of a row
+    const int t = tid & 127;
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
+      for (int j = 0; j < w.kt1 - w.kt0 && go; ++j, ++c) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = kv ? VS : KS;
+          go = __all_sync(0xffffffffu, wait(&raw_full[(c % RS) * 2 + kv], (uint32_t)(c / RS) & 1u) &&
+                                           (c < n || wait((kv ? vempty : kempty) + c % n, (uint32_t)(c / n - 1) & 1u)));
+          if (!go) break;
+          const unsigned char* src = sm + S::off_raw + ((c % RS) * 2 + kv) * S::kRaw;
+          unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile;
+          ex_s[(c & 3) * 256 + kv * 128 + t] = src[128 * D + t];
+          constexpr uint32_t f = 0x7b807b80u;  // 2^120 twice: the codes' own values (the exponents go to the softmax)
+#pragma unroll 4
+          for (int i = t; i < 128 * CPR; i += 128) {
+            const int row = i / CPR, ch = i % CPR;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + i * 16);
+            uint4 o0, o1;
+            e4m3x4_bf16(v.x, f, o0.x, o0.y);
+            e4m3x4_bf16(v.y, f, o0.z, o0.w);
+            e4m3x4_bf16(v.z, f, o1.x, o1.y);
+            e4m3x4_bf16(v.w, f, o1.z, o1.w);
+            const bool swap = D == 128 && (ch & 4);  // (see the kernel of many rows)
+            const int c0 = 2 * ch + (swap ? 1 : 0), c1 = 2 * ch + (swap ? 0 : 1);
+            unsigned char* d = dst + (ch >> 2) * kHalfBytes;
+            *reinterpret_cast<uint4*>(d + sw_off(row, c0)) = swap ? o1 : o0;
+            *reinterpret_cast<uint4*>(d + sw_off(row, c1)) = swap ? o0 : o1;
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[(c % RS) * 2 + kv]);
+            mbar_arrive(&(kv ? vfull : kfull)[c % n]);
+          }
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 256);
+}
+
+template <int D, int RQ, bool Q8>
+cudaError_t launch_few(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
+  using S = FewSmem<D, RQ, Q8>;
+  cudaError_t e = set_smem_once<pool_few_kernel<D, RQ, Q8>>(S::bytes);
+  if (e == cudaSuccess && a.planned) e = launch_plan<RQ, kKT>(a, st);
+  if (e != cudaSuccess) return e;
+  PoolMaps none = {};
+  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 384 : 256, S::bytes, st>>>(maps ? *maps : none, a);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, RQ, kKT>(a, st);
+}
+
+template <int D, bool Q8>
+cudaError_t launch_few_d(const PoolAttendArgs& a, const PoolMaps* maps, int TM, cudaStream_t st) {
+  switch (TM) {
+    case 8: return launch_few<D, 8, Q8>(a, maps, st);
+    case 16: return launch_few<D, 16, Q8>(a, maps, st);
+    case 32: return launch_few<D, 32, Q8>(a, maps, st);
+    default: return launch_few<D, 64, Q8>(a, maps, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pool_few(const PoolAttendArgs& a, const PoolMaps* maps, int TM, int bits, int d, cudaStream_t stream) {
+  if (d == 64) return bits == 8 ? launch_few_d<64, true>(a, maps, TM, stream) : launch_few_d<64, false>(a, maps, TM, stream);
+  return bits == 8 ? launch_few_d<128, true>(a, maps, TM, stream) : launch_few_d<128, false>(a, maps, TM, stream);
+}
+
+}  // namespace lod
