@@ -15,28 +15,27 @@ struct FewSmem {
   static constexpr int KS = kWide * (Q8 ? 1 : RQ == 64 ? 2 : 3);
   static constexpr int VS = kWide * (Q8 ? (RQ == 64 ? 1 : 2) : RQ >= 32 ? 2 : 3);
   static constexpr int RS = kWide * (RQ >= 32 ? 2 : 3);  // stages of codes (K and V of a tile)
-  static constexpr int kRaw = 128 * D + 128;
+  static constexpr int kRaw = 128 * D;
   static constexpr int kQ = NQ * D * 2, kP = NQ * 256;
   static constexpr size_t off_V = 0;  // (with d = 64 MMA 2 reads one tile past a V tile: K tiles follow)
   static constexpr size_t off_K = off_V + (size_t)VS * kTile;
   static constexpr size_t off_P = off_K + (size_t)KS * kTile;  // [2][2 key halves][NQ][128 B]
   static constexpr size_t off_Q = off_P + 2 * kP;              // [2][D / 64 halves][NQ][128 B]
   static constexpr size_t off_raw = off_Q + 2 * kQ;
-  static constexpr size_t off_ex = off_raw + (Q8 ? (size_t)RS * 2 * kRaw : 0);  // uint8 [4][2][128]
-  static constexpr size_t off_m = off_ex + (Q8 ? 1024 : 0);                     // float [NQ]
+  static constexpr size_t off_ex = off_raw + (Q8 ? (size_t)RS * 2 * kRaw : 0);  // uint8 [16][2][128]
+  static constexpr size_t off_m = off_ex + (Q8 ? 16 * 256 : 0);                 // float [NQ]
   static constexpr size_t off_red = off_m + 4 * 64;                             // float [4][64]
   static constexpr size_t off_pos = off_red + 4 * 4 * 64;                       // int2 [64]
   static constexpr size_t off_info = off_pos + 8 * 64;                          // uint32 [16]
   static constexpr size_t off_wb = off_info + 64;                               // int64 [kInlineSeqs + 1]
-  static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 1;
+  static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 2;
   static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
   static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  // exponent bytes are kept for 4 tiles: the codes' warps run at most KS + 2
-  // (K) and VS (V) tiles ahead of the softmax; block masks for 16: the copies
-  // run at most RS tiles ahead of those (8-bit), or KS, VS ahead
-  static_assert(!Q8 || (KS <= 2 && VS <= 4), "exponent ring");
-  static_assert(RS + VS + 2 <= 16, "block mask ring");
+  // block masks and exponent bytes are kept for 16 tiles: the copies run at
+  // most RS tiles ahead of the codes' warps, and those (or, without codes,
+  // the copies) KS + 2 (K) or VS (V) tiles ahead of the softmax
+  static_assert(RS + (KS + 2 > VS ? KS + 2 : VS) < 16, "ring of block masks and exponents");
 };
 
 // The cache is the A operand: S^T = K Q^T (M = 128 keys, N = query rows), so
@@ -46,12 +45,14 @@ struct FewSmem {
 // taken against a reference maximum per query row; only when some score
 // exceeds it by more than 2^8 (and on a unit's first tile) does the
 // warpgroup find new maxima and rescale O^T.
-// Roles: warp 0 TMA copies, warp 1 MMA issue, warps 2 and 3 query tiles,
-// warps 4-7 softmax, with an 8-bit pool warps 8-11 codes to bf16.
+// Roles: warp 0 copies, warp 1 the MMAs of S^T, warp 2 those of O^T (two
+// issuers: neither waits for the other's operands), warp 3 query tiles, warps
+// 4-7 softmax, with an 8-bit pool warps 8-11 and 12-15 codes to bf16
+// (keys, values).
 // Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
 // HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
 template <int D, int RQ, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
+__global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
     pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
   using S = FewSmem<D, RQ, Q8>;
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
   uint64_t* pv_done = p_ready + 2;
   uint64_t* q_full = pv_done + 2;
   uint64_t* q_empty = q_full + 2;
-  uint64_t* fin = q_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  uint64_t* fin = q_empty + 2;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* m_s = reinterpret_cast<float*>(sm + S::off_m);
   float* red_s = reinterpret_cast<float*>(sm + S::off_red);
@@ -100,10 +101,10 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
       mbar_init(&s_free[i], 4);
       mbar_init(&p_ready[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&q_full[i], 2);
+      mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+      mbar_init(&fin[i], 1);
     }
-    mbar_init(fin, 1);
     *abort_s = 0;
     fence_mbar_init();
     if (!Q8) {
@@ -127,41 +128,22 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t kColO = 128;  // S^T in columns [0, 64) and [64, 128)
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_s) return false;
-    if (mbar_wait(bar, parity, a.status)) return true;
-    *abort_s = 1;
-    return false;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, abort_s, a.status); };
   // wait for use number `i` of a ring of n barriers
   auto wait_ring = [&](uint64_t* bars, int n, int i) { return wait(&bars[i % n], (uint32_t)(i / n) & 1u); };
   const int shift = a.pool.shift;
   const int per_tile = kKT >> shift;
   const uint32_t all_ok = (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1);
 
+  if (Q8 && warp < 4) regs_dec<72>();
   if (warp == 0) {
     // ============================================================== copies
     int c = 0;  // key tiles
     bool go = true;
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
-      const int32_t* table = a.batch.table + (int64_t)w.u.b * a.batch.max_blocks;
-      const int nblk = (int)((w.s.len + (1 << shift) - 1) >> shift);
-      int entry = -1;  // this lane's block of the next key tile
-      auto load_entry = [&](int kt) {
-        const int i = kt * per_tile + lane;
-        entry = -1;
-        if (lane < per_tile && i < nblk && kt < w.kt1) {
-          entry = table[i];
-          if (entry < 0 || entry >= a.pool.blocks) {
-            set_status(a.status, LOD_ST_BAD_PAGE);
-            entry = -1;
-          }
-        }
-      };
-      load_entry(w.kt0);
-      for (int kt = w.kt0; kt < w.kt1 && go; ++kt, ++c) {
-        const int mine = entry;
-        load_entry(kt + 1);
+      Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
+      for (int kt = w.kt0; kt < w.kt1 && go; f.advance(kt), ++kt, ++c) {
+        const int mine = f.cur;
         const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
         const int rows = __popc(ok) << shift;
         const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
@@ -172,17 +154,17 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
             uint64_t* bar = &raw_full[(c % RS) * 2 + kv];
             if (c >= RS && !(go = wait(&raw_empty[(c % RS) * 2 + kv], (uint32_t)(c / RS - 1) & 1u))) break;
             unsigned char* dst = sm + S::off_raw + ((c % RS) * 2 + kv) * S::kRaw;
+            if (lane < 16 && (lane >> 3) == kv) *reinterpret_cast<uint4*>(ex_s + (c & 15) * 256 + lane * 16) = f.ex;
+            if (kv == 0 && lane == 0) info_s[c & 15] = ok;
+            __syncwarp();
             if (lane == 0) {
-              if (kv == 0) info_s[c & 15] = ok;
-              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * (D + 1));
+              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * D);
               else mbar_arrive(bar);
             }
             __syncwarp();
             if (mine >= 0) {
               const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-              const uint8_t* ex = kv ? a.pool.Ve : a.pool.Ke;
               bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, bar);
-              bulk_g2s(dst + 128 * D + (lane << shift), ex + row, 1u << shift, bar);
             }
           } else {
             const int n = kv ? VS : KS, st = c % n;
@@ -216,62 +198,71 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
       }
     }
   } else if (warp == 1) {
-    // ============================================================== MMA issue
+    // ============================================================== S^T = K Q^T
     if (lane == 0) {
       const uint32_t idS = tc::idesc_bf16(128, NQ, false, false);
-      const uint32_t idO = tc::idesc_bf16(128, NQ, true, false);
-      const uint32_t qb = smem_u32(sm + S::off_Q), pb = smem_u32(sm + S::off_P);
-      const uint32_t kb = smem_u32(sm + S::off_K), vb = smem_u32(sm + S::off_V);
+      const uint32_t qb = smem_u32(sm + S::off_Q), kb = smem_u32(sm + S::off_K);
       int c = 0, k = 0;  // key tiles, units
-      bool go = true, any = false;
-      auto values = [&](int x, bool acc) -> bool {  // O^T (+)= V_x^T P_x^T
-        if (!wait_ring(p_ready, 2, x) || !wait_ring(vfull, VS, x)) return false;
-        tc::fence_after_sync();
-        const uint32_t vs = vb + (uint32_t)(x % VS) * S::kTile, ps = pb + (uint32_t)(x & 1) * S::kP;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16(tmem + kColO, tc::desc_mnmajor_sw128(vs + kk * 2048, kHalfBytes),
-                       tc::desc_kmajor_sw128(ps + (kk >> 2) * NQ * 128 + (kk & 3) * 32), idO, acc || kk > 0);
-        tc::mma_commit(&vempty[x % VS]);
-        tc::mma_commit(&pv_done[x & 1]);
-        return true;
-      };
+      bool go = true;
       for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
         if (!(go = wait_ring(q_full, 2, k))) break;
-        const uint32_t qs = qb + (uint32_t)(k & 1) * S::kQ;
+        const uint64_t qd = tc::desc_kmajor_sw128(qb + (uint32_t)(k & 1) * S::kQ);
         const int T = w.kt1 - w.kt0;
-        for (int j = 0; j < T && go; ++j, ++c) {
-          if (!(go = wait_ring(kfull, KS, c))) break;
-          if (c >= 2 && !(go = wait_ring(s_free, 2, c - 2))) break;
+        for (int j = 0; j < T; ++j, ++c) {
+          if (!(go = (c < 2 || wait_ring(s_free, 2, c - 2)) && wait_ring(kfull, KS, c))) break;
           tc::fence_after_sync();
-          const uint32_t ks = kb + (uint32_t)(c % KS) * S::kTile;
+          const uint64_t kd = tc::desc_kmajor_sw128(kb + (uint32_t)(c % KS) * S::kTile);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_bf16(tmem + (c & 1) * 64, tc::desc_kmajor_sw128(ks + (kk >> 2) * kHalfBytes + (kk & 3) * 32),
-                         tc::desc_kmajor_sw128(qs + (kk >> 2) * NQ * 128 + (kk & 3) * 32), idS, kk > 0);
-          tc::mma_commit(&kempty[c % KS]);
+          for (int kk = 0; kk < D / 16; ++kk)  // (the address field of a descriptor counts 16 bytes)
+            tc::mma_bf16(tmem + (c & 1) * 64, kd + (((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4),
+                         qd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idS, kk > 0);
           tc::mma_commit(&s_full[c & 1]);
+          tc::mma_commit(&kempty[c % KS]);
           if (j == T - 1) tc::mma_commit(&q_empty[k & 1]);
-          any = true;
-          if (j > 0) go = values(c - 1, j > 1);
-          if (go && j == T - 1) go = values(c, j > 0);
         }
       }
-      if (any) {
-        tc::mma_commit(fin);
-        (void)mbar_wait(fin, 0, a.status);
+      if (c > 0) {
+        tc::mma_commit(&fin[0]);
+        (void)mbar_wait(&fin[0], 0, a.status);
       }
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // ============================================================== O^T += V^T P^T
+    if (lane == 0) {
+      const uint32_t idO = tc::idesc_bf16(128, NQ, true, false);
+      const uint32_t pb = smem_u32(sm + S::off_P), vb = smem_u32(sm + S::off_V);
+      int c = 0;
+      bool go = true;
+      for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
+        const int T = w.kt1 - w.kt0;
+        for (int j = 0; j < T; ++j, ++c) {
+          if (!(go = wait_ring(vfull, VS, c) && wait_ring(p_ready, 2, c))) break;
+          tc::fence_after_sync();
+          const uint64_t vd = tc::desc_mnmajor_sw128(vb + (uint32_t)(c % VS) * S::kTile, kHalfBytes);
+          const uint64_t pd = tc::desc_kmajor_sw128(pb + (uint32_t)(c & 1) * S::kP);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_bf16(tmem + kColO, vd + kk * (2048 >> 4), pd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idO,
+                         j > 0 || kk > 0);
+          tc::mma_commit(&pv_done[c & 1]);
+          tc::mma_commit(&vempty[c % VS]);
+        }
+      }
+      if (c > 0) {
+        tc::mma_commit(&fin[1]);
+        (void)mbar_wait(&fin[1], 0, a.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
     // ============================================================== query tiles
     int k = 0;
     bool go = true;
-    const int r0 = tid - 64;
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
       if (k >= 2 && !(go = __all_sync(0xffffffffu, wait_ring(q_empty, 2, k - 2)))) break;
       unsigned char* qs = sm + S::off_Q + (size_t)(k & 1) * S::kQ;
-      for (int x = r0; x < NQ * (D / 8); x += 64) {
+      for (int x = lane; x < NQ * (D / 8); x += 32) {
         const int r = x / (D / 8), ch = x % (D / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (r < w.nrow) {
@@ -287,6 +278,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
     }
   } else if (warp < 8) {
     // ============================================================== softmax
+    if (Q8) regs_inc<248>();
     const int r = tid & 127;  // key of the tile; channel of O^T
     const int q4 = warp & 3;
     const uint32_t tl = (uint32_t)(32 * q4) << 16;
@@ -315,14 +307,15 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
       for (int n = 0; n < RQ; ++n) l[n] = 0.f;
       for (int j = 0; j < T; ++j, ++c) {
         const int k0 = (w.kt0 + j) * kKT, t = k0 + r;
-        go = __all_sync(0xffffffffu, wait_ring(s_full, 2, c) && wait_ring(vfull, VS, c));
+        go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
+                                         wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
         const uint32_t ok = info_s[c & 15];
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
         const bool live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
         float ks = a.scale_log2, vs = 1.f;
         if constexpr (Q8) {
-          const int e0 = ex_s[(c & 3) * 256 + r], e1 = ex_s[(c & 3) * 256 + 128 + r];
+          const int e0 = ex_s[(c & 15) * 256 + r], e1 = ex_s[(c & 15) * 256 + 128 + r];
           ks *= e0 == 255 ? NAN : __uint_as_float((uint32_t)max(e0, 7) << 23);
           vs = e1 == 255 ? NAN : __uint_as_float((uint32_t)max(e1, 7) << 23);
         } else if (masked && go && (!live || t < first_lo)) {
@@ -403,7 +396,6 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
           }
         }
         // weights
-        if (c >= 2) go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 2));
         unsigned char* P = sm + S::off_P + (size_t)(c & 1) * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
         const int ch = (r & 63) >> 3;
 #pragma unroll
@@ -466,43 +458,27 @@ __global__ void __launch_bounds__(Q8 ? 384 : 256, 1)
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to bf16 tiles
+    regs_dec<96>();
     int c = 0;
     bool go = true;
-    constexpr int CPR = D / 16;  // 16-code chunks of a row
-    const int t = tid & 127;
+    const int t = tid & 127, kv = (warp - 8) >> 2;
+    const int n = kv ? VS : KS;
+    uint64_t* full = kv ? vfull : kfull;
+    uint64_t* empty = kv ? vempty : kempty;
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
-      for (int j = 0; j < w.kt1 - w.kt0 && go; ++j, ++c) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int n = kv ? VS : KS;
-          go = __all_sync(0xffffffffu, wait(&raw_full[(c % RS) * 2 + kv], (uint32_t)(c / RS) & 1u) &&
-                                           (c < n || wait((kv ? vempty : kempty) + c % n, (uint32_t)(c / n - 1) & 1u)));
-          if (!go) break;
-          const unsigned char* src = sm + S::off_raw + ((c % RS) * 2 + kv) * S::kRaw;
-          unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile;
-          ex_s[(c & 3) * 256 + kv * 128 + t] = src[128 * D + t];
-          constexpr uint32_t f = 0x7b807b80u;  // 2^120 twice: the codes' own values (the exponents go to the softmax)
-#pragma unroll 4
-          for (int i = t; i < 128 * CPR; i += 128) {
-            const int row = i / CPR, ch = i % CPR;
-            const uint4 v = *reinterpret_cast<const uint4*>(src + i * 16);
-            uint4 o0, o1;
-            e4m3x4_bf16(v.x, f, o0.x, o0.y);
-            e4m3x4_bf16(v.y, f, o0.z, o0.w);
-            e4m3x4_bf16(v.z, f, o1.x, o1.y);
-            e4m3x4_bf16(v.w, f, o1.z, o1.w);
-            const bool swap = D == 128 && (ch & 4);  // (see the kernel of many rows)
-            const int c0 = 2 * ch + (swap ? 1 : 0), c1 = 2 * ch + (swap ? 0 : 1);
-            unsigned char* d = dst + (ch >> 2) * kHalfBytes;
-            *reinterpret_cast<uint4*>(d + sw_off(row, c0)) = swap ? o1 : o0;
-            *reinterpret_cast<uint4*>(d + sw_off(row, c1)) = swap ? o0 : o1;
-          }
-          tc::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[(c % RS) * 2 + kv]);
-            mbar_arrive(&(kv ? vfull : kfull)[c % n]);
-          }
+      for (int j = 0; j < w.kt1 - w.kt0; ++j, ++c) {
+        const int raw = (c % RS) * 2 + kv;
+        go = __all_sync(0xffffffffu, wait(&raw_full[raw], (uint32_t)(c / RS) & 1u) &&
+                                         (c < n || wait(&empty[c % n], (uint32_t)(c / n - 1) & 1u)));
+        if (!go) break;
+        const unsigned char* src = sm + S::off_raw + raw * S::kRaw;
+        unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile;
+        convert_tile<D, false>(src, nullptr, dst, t);  // (the softmax multiplies by the powers of two)
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[raw]);
+          mbar_arrive(&full[c % n]);
         }
       }
     }
@@ -517,10 +493,12 @@ template <int D, int RQ, bool Q8>
 cudaError_t launch_few(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
   using S = FewSmem<D, RQ, Q8>;
   cudaError_t e = set_smem_once<pool_few_kernel<D, RQ, Q8>>(S::bytes);
+  // 128 (72 + 248 + 96 + 96) = 512 * 128
+  if (e == cudaSuccess && Q8) e = check_registers<pool_few_kernel<D, RQ, Q8>>(128);
   if (e == cudaSuccess && a.planned) e = launch_plan<RQ, kKT>(a, st);
   if (e != cudaSuccess) return e;
   PoolMaps none = {};
-  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 384 : 256, S::bytes, st>>>(maps ? *maps : none, a);
+  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 512 : 256, S::bytes, st>>>(maps ? *maps : none, a);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, RQ, kKT>(a, st);
 }

@@ -89,12 +89,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   const uint32_t tmem = *tmem_slot;
   constexpr uint32_t kColO = 256;
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (*abort_s) return false;
-    if (mbar_wait(bar, parity, a.status)) return true;
-    *abort_s = 1;
-    return false;
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, abort_s, a.status); };
   const int shift = a.pool.shift;
   const int per_tile = kKT >> shift;  // blocks of a key tile
 
@@ -106,24 +101,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       int c = 0;  // tiles copied (K and V count apart)
       bool go = true;
       for (; w.more() && go; w.next()) {
-        const int32_t* table = a.batch.table + (int64_t)w.u.b * a.batch.max_blocks;
-        const int nblk = (int)((w.s.len + (1 << shift) - 1) >> shift);
-        int entry = -1;  // this lane's block of the next key tile
-        auto load_entry = [&](int kt) {
-          const int i = kt * per_tile + lane;
-          entry = -1;
-          if (lane < per_tile && i < nblk && kt < w.kt1) {
-            entry = table[i];
-            if (entry < 0 || entry >= a.pool.blocks) {
-              set_status(a.status, LOD_ST_BAD_PAGE);
-              entry = -1;
-            }
-          }
-        };
-        load_entry(w.kt0);
-        for (int kt = w.kt0; kt < w.kt1 && go; ++kt) {
-          const int mine = entry;
-          load_entry(kt + 1);
+        Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
+        for (int kt = w.kt0; kt < w.kt1 && go; f.advance(kt), ++kt) {
+          const int mine = f.cur;
           const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
           const int rows = __popc(ok) << shift;
           const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
@@ -133,16 +113,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
               const int st = c & 1;
               if (c >= 2 && !(go = wait(&raw_empty[st], (uint32_t)((c - 2) >> 1) & 1u))) break;
               unsigned char* dst = sm + S::off_raw + st * S::kRaw;
+              if (lane < 16 && (lane >> 3) == kv) *reinterpret_cast<uint4*>(dst + 128 * D + (lane & 7) * 16) = f.ex;
+              __syncwarp();
               if (lane == 0) {
-                if (rows) mbar_arrive_expect(&raw_full[st], (uint32_t)rows * (D + 1));
+                if (rows) mbar_arrive_expect(&raw_full[st], (uint32_t)rows * D);
                 else mbar_arrive(&raw_full[st]);
               }
               __syncwarp();
               if (mine >= 0) {
                 const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-                const uint8_t* ex = kv ? a.pool.Ve : a.pool.Ke;
                 bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, &raw_full[st]);
-                bulk_g2s(dst + 128 * D + (lane << shift), ex + row, 1u << shift, &raw_full[st]);
               }
             } else {
               const int st = c % NS;
@@ -181,11 +161,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         bool go = true, any = false;
         auto full_wait = [&](int x) { return wait(&full[x % NS], (uint32_t)(x / NS) & 1u); };
         auto scores = [&](int s, int x) {  // S_s = Q_s K^T, K at ring position x
-          const uint32_t qs = qb + s * S::kTile, ks = kvb + (uint32_t)(x % NS) * S::kTile;
+          const uint64_t qd = tc::desc_kmajor_sw128(qb + s * S::kTile);
+          const uint64_t kd = tc::desc_kmajor_sw128(kvb + (uint32_t)(x % NS) * S::kTile);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-            tc::mma_bf16(tmem + s * 128, tc::desc_kmajor_sw128(qs + o), tc::desc_kmajor_sw128(ks + o), idS, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {  // (the address field of a descriptor counts 16 bytes)
+            const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+            tc::mma_bf16(tmem + s * 128, qd + o, kd + o, idS, kk > 0);
           }
           tc::mma_commit(&s_full[s]);
           any = true;
@@ -203,11 +184,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
               if (!(go = wait(&p_ready[s], np[s]++ & 1u))) break;
               if (s == 0 && !(go = full_wait(c + 1))) break;
               tc::fence_after_sync();
-              const uint32_t vs = kvb + (uint32_t)((c + 1) % NS) * S::kTile;
+              const uint64_t vd = tc::desc_mnmajor_sw128(kvb + (uint32_t)((c + 1) % NS) * S::kTile, kHalfBytes);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc::mma_bf16_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * kk,
-                                tc::desc_mnmajor_sw128(vs + kk * 2048, kHalfBytes), idO, j > 0 || kk > 0);
+                tc::mma_bf16_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * kk, vd + kk * (2048 >> 4), idO,
+                                j > 0 || kk > 0);
               if (s == tiles - 1) tc::mma_commit(&empty[(c + 1) % NS]);
               if (j + 1 < T) {
                 if (s == 0 && !(go = full_wait(c + 2))) break;
@@ -404,7 +385,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     regs_dec<72>();
     int c = 0;
     bool go = true;
-    constexpr int CPR = D / 16;  // 16-code chunks of a row
     for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
       for (int x = 0; x < 2 * (w.kt1 - w.kt0); ++x, ++c) {
         go = __all_sync(0xffffffffu, wait(&raw_full[c & 1], (uint32_t)(c >> 1) & 1u) &&
@@ -412,26 +392,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         if (!go) break;
         const unsigned char* src = sm + S::off_raw + (c & 1) * S::kRaw;
         unsigned char* dst = sm + S::off_KV + (size_t)(c % NS) * S::kTile;
-        const int t = tid & 127;
-#pragma unroll 2
-        for (int i = t; i < 128 * CPR; i += 128) {
-          const int row = i / CPR, ch = i % CPR;
-          const uint4 v = *reinterpret_cast<const uint4*>(src + i * 16);
-          uint32_t f1, f2;
-          e4m3_factors(src[128 * D + row], f1, f2);
-          uint4 o0, o1;
-          e4m3x4_bf16(v.x, f1, f2, o0.x, o0.y);
-          e4m3x4_bf16(v.y, f1, f2, o0.z, o0.w);
-          e4m3x4_bf16(v.z, f1, f2, o1.x, o1.y);
-          e4m3x4_bf16(v.w, f1, f2, o1.z, o1.w);
-          // a row's two halves lie on the same banks: the lanes of the second
-          // half store their two chunks in the other order
-          const bool swap = D == 128 && (ch & 4);
-          const int c0 = 2 * ch + (swap ? 1 : 0), c1 = 2 * ch + (swap ? 0 : 1);
-          unsigned char* d = dst + (ch >> 2) * kHalfBytes;
-          *reinterpret_cast<uint4*>(d + sw_off(row, c0)) = swap ? o1 : o0;
-          *reinterpret_cast<uint4*>(d + sw_off(row, c1)) = swap ? o0 : o1;
-        }
+        convert_tile<D, true>(src, src + 128 * D, dst, tid & 127);
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
