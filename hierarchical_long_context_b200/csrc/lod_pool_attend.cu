@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
     const int64_t row0 = u.i * TM, rows = (int64_t)s.n * a.G;
     const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
     const int32_t* table = a.batch.table + (int64_t)u.b * a.batch.max_blocks;
+    const int64_t first_unit = a.window > 0 ? s.len - s.n + row0 / a.G - a.window + 1 : 0;  // (earlier keys: no row's)
 
     __syncthreads();
     for (int x = tid; x < TM * PPR; x += NT) {
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
         const int k = x / PPR, c = x % PPR;
         const int64_t t = (int64_t)kt * KT + k;
         int64_t blk = -1;
-        if (t < s.len) {
+        if (t < s.len && t >= first_unit) {
           blk = table[t >> a.pool.shift];
           if (blk < 0 || blk >= a.pool.blocks) {
             blk = -1;

@@ -25,14 +25,16 @@ struct FewSmem {
   static constexpr size_t off_ex = off_raw + (Q8 ? (size_t)RS * 2 * kRaw : 0);  // uint8 [16][2][128]
   static constexpr size_t off_m = off_ex + (Q8 ? 16 * 256 : 0);                 // float [NQ]
   static constexpr size_t off_red = off_m + 4 * 64;                             // float [4][64]
-  static constexpr size_t off_pos = off_red + 4 * 4 * 64;                       // int2 [64]
-  static constexpr size_t off_info = off_pos + 8 * 64;                          // uint32 [16]
-  static constexpr size_t off_wb = off_info + 64;                               // int64 [kInlineSeqs + 1]
+  static constexpr size_t off_qe = off_red + 4 * 4 * 64;                        // float [16][NQ]
+  static constexpr size_t off_pos = off_qe + (Q8 ? 16 * 4 * NQ : 0);                       // int2 [64]
+  static constexpr size_t off_info = off_pos + 8 * 64;                          // uint2 [16]
+  static constexpr size_t off_wb = off_info + 128;                               // int64 [kInlineSeqs + 1]
   static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 2;
   static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
   static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-  // block masks and exponent bytes are kept for 16 tiles: the copies run at
+  // block masks, exponent bytes and query scales are kept for 16 tiles (units
+  // have one at least): the copies run at
   // most RS tiles ahead of the codes' warps, and those (or, without codes,
   // the copies) KS + 2 (K) or VS (V) tiles ahead of the softmax
   static_assert(RS + (KS + 2 > VS ? KS + 2 : VS) < 16, "ring of block masks and exponents");
@@ -45,9 +47,13 @@ struct FewSmem {
 // taken against a reference maximum per query row; only when some score
 // exceeds it by more than 2^8 (and on a unit's first tile) does the
 // warpgroup find new maxima and rescale O^T.
-// Roles: warp 0 copies, warp 1 the MMAs of S^T, warp 2 those of O^T (two
-// issuers: neither waits for the other's operands), warp 3 query tiles, warps
-// 4-7 softmax, with an 8-bit pool warps 8-11 and 12-15 codes to bf16
+// With an 8-bit pool the weight of a key carries its value row's exponent,
+// w = 2^(score + e_v - m) with m the running maximum of score + e_v: the
+// codes then enter the MMA as they are, and w fills f16's range from the top,
+// so what f16 drops lies 2^-30 below the largest weighted value.
+// Roles: warp 0 copies of keys, warp 1 the MMAs of S^T, warp 2 those of O^T
+// (two issuers: neither waits for the other's operands), warp 3 query tiles
+// and copies of values, warps 4-7 softmax, with an 8-bit pool warps 8-11 and 12-15 codes to bf16
 // (keys, values).
 // Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
 // HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
@@ -57,6 +63,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   using S = FewSmem<D, RQ, Q8>;
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
   constexpr float kTau = 8.f;
+  constexpr float kUp = 6.f;  // 8-bit: weights are up to 2^14 of f16's 2^16
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -78,7 +85,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   float* m_s = reinterpret_cast<float*>(sm + S::off_m);
   float* red_s = reinterpret_cast<float*>(sm + S::off_red);
   int2* pos_s = reinterpret_cast<int2*>(sm + S::off_pos);
-  volatile uint32_t* info_s = reinterpret_cast<volatile uint32_t*>(sm + S::off_info);
+  uint2* info_s = reinterpret_cast<uint2*>(sm + S::off_info);  // blocks that are there, largest value exponent
+  float* qe_s = reinterpret_cast<float*>(sm + S::off_qe);
   unsigned char* ex_s = sm + S::off_ex;
   int64_t* wb_s = reinterpret_cast<int64_t*>(sm + S::off_wb);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -135,72 +143,70 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   const int per_tile = kKT >> shift;
   const uint32_t all_ok = (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1);
 
-  if (Q8 && warp < 4) regs_dec<72>();
-  if (warp == 0) {
-    // ============================================================== copies
-    int c = 0;  // key tiles
-    bool go = true;
-    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
-      Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
-      for (int kt = w.kt0; kt < w.kt1 && go; f.advance(kt), ++kt, ++c) {
-        const int mine = f.cur;
-        const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
-        const int rows = __popc(ok) << shift;
-        const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
-        if (!Q8 && lane == 0) info_s[c & 15] = ok;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if constexpr (Q8) {
-            uint64_t* bar = &raw_full[(c % RS) * 2 + kv];
-            if (c >= RS && !(go = wait(&raw_empty[(c % RS) * 2 + kv], (uint32_t)(c / RS - 1) & 1u))) break;
-            unsigned char* dst = sm + S::off_raw + ((c % RS) * 2 + kv) * S::kRaw;
-            if (lane < 16 && (lane >> 3) == kv) *reinterpret_cast<uint4*>(ex_s + (c & 15) * 256 + lane * 16) = f.ex;
-            if (kv == 0 && lane == 0) info_s[c & 15] = ok;
-            __syncwarp();
-            if (lane == 0) {
-              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * D);
-              else mbar_arrive(bar);
-            }
-            __syncwarp();
-            if (mine >= 0) {
-              const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-              bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, bar);
-            }
-          } else {
-            const int n = kv ? VS : KS, st = c % n;
-            uint64_t* bar = (kv ? vfull : kfull) + st;
-            if (c >= n && !(go = wait((kv ? vempty : kempty) + st, (uint32_t)(c / n - 1) & 1u))) break;
-            unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)st * S::kTile;
-            if (lane == 0) {
-              if (rows) mbar_arrive_expect(bar, (uint32_t)rows * D * 2);
-              else mbar_arrive(bar);
-            }
-            __syncwarp();
-            if (mine >= 0) {
-              const CUtensorMap* map = kv ? &maps.V : &maps.K;
-              unsigned char* d = dst + (lane << shift) * 128;
-              tma_load_box(d, map, 0, (int)row, bar);
-              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, bar);
-            }
-          }
+  // The copies of a unit's keys (kv = 0) or values (kv = 1); `c` counts key
+  // tiles.  The values' warp also leaves each tile's block mask and, of an
+  // 8-bit pool, the exponent bytes of keys and values, before it announces
+  // the copy: the softmax waits for that one.
+  auto copies = [&](const Walk<RQ, kKT>& w, int kv, int& c) -> bool {
+    Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
+    const int n = Q8 ? RS : kv ? VS : KS;
+    for (int kt = w.kt0; kt < w.kt1; f.advance(kt), ++kt, ++c) {
+      const unsigned ok = __ballot_sync(0xffffffffu, f.cur >= 0);
+      const int rows = __popc(ok) << shift;
+      const int64_t row = ((int64_t)f.cur * a.pool.Hkv + w.u.h) << shift;
+      const int st = c % n;
+      uint64_t* full = Q8 ? &raw_full[st * 2 + kv] : (kv ? vfull : kfull) + st;
+      if (c >= n && !wait(Q8 ? &raw_empty[st * 2 + kv] : (kv ? vempty : kempty) + st, (uint32_t)(c / n - 1) & 1u))
+        return false;
+      if (kv == 1) {
+        int top = 0;
+        if (Q8) {
+          if (lane < 16) *reinterpret_cast<uint4*>(ex_s + (c & 15) * 256 + lane * 16) = f.ex;
+          top = __shfl_sync(0xffffffffu, f.largest(), 8);
+        }
+        if (lane == 0) info_s[c & 15] = make_uint2(ok, (uint32_t)top);
+        __syncwarp();
+      }
+      if (lane == 0) {
+        if (rows) mbar_arrive_expect(full, (uint32_t)rows * D * (Q8 ? 1 : 2));
+        else mbar_arrive(full);
+      }
+      __syncwarp();
+      if (f.cur >= 0) {
+        if constexpr (Q8) {
+          unsigned char* dst = sm + S::off_raw + (st * 2 + kv) * S::kRaw;
+          bulk_g2s(dst + (lane << shift) * D, static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K) + row * D,
+                   (uint32_t)D << shift, full);
+        } else {
+          const CUtensorMap* map = kv ? &maps.V : &maps.K;
+          unsigned char* d = sm + (kv ? S::off_V : S::off_K) + (size_t)st * S::kTile + (lane << shift) * 128;
+          tma_load_box(d, map, 0, (int)row, full);
+          if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, full);
         }
       }
     }
+    return true;
+  };
+  // after a wait has given up: copies still in flight land before the CTA ends
+  auto drain = [&](int kv, int c) {
     __syncwarp();
-    if (*abort_s && lane == 0) {  // copies still in flight land before the CTA ends
-      for (int kv = 0; kv < 2; ++kv) {
-        const int n = Q8 ? RS : kv ? VS : KS;
-        // (the last tile's copies may not have been issued: its barrier then
-        // times out once and the CTA ends)
-        for (int i = c - 1; i >= 0 && i >= c - n; --i)
-          (void)mbar_wait(Q8 ? &raw_full[(i % n) * 2 + kv] : (kv ? vfull : kfull) + i % n, (uint32_t)(i / n) & 1u,
-                          a.status);
-      }
-    }
+    if (!*abort_s || lane != 0) return;
+    const int n = Q8 ? RS : kv ? VS : KS;
+    for (int i = c - 1; i >= 0 && i >= c - n; --i)
+      (void)mbar_wait(Q8 ? &raw_full[(i % n) * 2 + kv] : (kv ? vfull : kfull) + i % n, (uint32_t)(i / n) & 1u, a.status);
+  };
+
+  if (Q8 && warp < 4) regs_dec<72>();
+  if (warp == 0) {
+    // ============================================================== keys
+    int c = 0;
+    bool go = true;
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) go = copies(w, 0, c);
+    drain(0, c);
   } else if (warp == 1) {
     // ============================================================== S^T = K Q^T
     if (lane == 0) {
-      const uint32_t idS = tc::idesc_bf16(128, NQ, false, false);
+      const uint32_t idS = Q8 ? idesc_f16(128, NQ, false, false) : tc::idesc_bf16(128, NQ, false, false);
       const uint32_t qb = smem_u32(sm + S::off_Q), kb = smem_u32(sm + S::off_K);
       int c = 0, k = 0;  // key tiles, units
       bool go = true;
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   } else if (warp == 2) {
     // ============================================================== O^T += V^T P^T
     if (lane == 0) {
-      const uint32_t idO = tc::idesc_bf16(128, NQ, true, false);
+      const uint32_t idO = Q8 ? idesc_f16(128, NQ, true, false) : tc::idesc_bf16(128, NQ, true, false);
       const uint32_t pb = smem_u32(sm + S::off_P), vb = smem_u32(sm + S::off_V);
       int c = 0;
       bool go = true;
@@ -256,26 +262,50 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ============================================================== query tiles
-    int k = 0;
+    // ============================================================== query tiles, values
+    int k = 0, c = 0;
     bool go = true;
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
       if (k >= 2 && !(go = __all_sync(0xffffffffu, wait_ring(q_empty, 2, k - 2)))) break;
       unsigned char* qs = sm + S::off_Q + (size_t)(k & 1) * S::kQ;
-      for (int x = lane; x < NQ * (D / 8); x += 32) {
-        const int r = x / (D / 8), ch = x % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < w.nrow) {
-          const int g = (int)w.u.i * RQ + r;
-          v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + g / a.G) * a.qt +
-                                              (int64_t)(w.u.h * a.G + g % a.G) * a.qh + ch * 8);
+      auto row_of = [&](int r) {
+        const int g = (int)w.u.i * RQ + r;
+        return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + g / a.G) * a.qt +
+                                              (int64_t)(w.u.h * a.G + g % a.G) * a.qh);
+      };
+      if constexpr (Q8) {  // a row is a group of D / 8 lanes, 16 bytes each
+        constexpr int LPR = D / 8;
+        for (int r = lane / LPR; r < NQ; r += 32 / LPR) {
+          const int ch = lane % LPR;
+          uint4 v = r < w.nrow ? row_of(r)[ch] : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = query_exponent(top);
+          const float f = exp2i(-e);
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = pack_f16x2(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * NQ * 128 + sw_off(r, ch)) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (ch == 0) qe_s[(k & 15) * NQ + r] = exp2i(e);
         }
-        *reinterpret_cast<uint4*>(qs + (ch >> 3) * NQ * 128 + sw_off(r, ch)) = v;
+      } else {
+        for (int x = lane; x < NQ * (D / 8); x += 32) {
+          const int r = x / (D / 8), ch = x % (D / 8);
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * NQ * 128 + sw_off(r, ch)) =
+              r < w.nrow ? row_of(r)[ch] : make_uint4(0, 0, 0, 0);
+        }
       }
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[k & 1]);
+      go = copies(w, 1, c);
     }
+    drain(1, c);
   } else if (warp < 8) {
     // ============================================================== softmax
     if (Q8) regs_inc<248>();
@@ -287,10 +317,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
       if constexpr (CH == 8) tc::tmem_ld8(at, v);
       else tc::tmem_ld16(at, v);
     };
-    int c = 0;
+    int c = 0, k = 0;
     bool go = true;
-    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
+      const float* qe = qe_s + (k & 15) * NQ;
+      float cv = 0.f;  // (8-bit) the unit's value exponent: sums of weights are in units of 2^cv
       const int p0 = (int)(w.s.len - w.s.n), g0 = (int)w.u.i * RQ;
       const int pos_lo = p0 + g0 / a.G, pos_hi = p0 + (g0 + w.nrow - 1) / a.G;
       auto first_of = [&](int pos) { return a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0; };
@@ -310,15 +342,20 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
         go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
                                          wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
-        const uint32_t ok = info_s[c & 15];
+        const uint2 info = info_s[c & 15];
+        const uint32_t ok = info.x;
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
         const bool live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
-        float ks = a.scale_log2, vs = 1.f;
+        float ks = a.scale_log2, ve = 0.f, pe = 1.f;
         if constexpr (Q8) {
+          // (rows of exponent 255 hold NaN codes: any factor will do)
           const int e0 = ex_s[(c & 15) * 256 + r], e1 = ex_s[(c & 15) * 256 + 128 + r];
-          ks *= e0 == 255 ? NAN : __uint_as_float((uint32_t)max(e0, 7) << 23);
-          vs = e1 == 255 ? NAN : __uint_as_float((uint32_t)max(e1, 7) << 23);
-        } else if (masked && go && (!live || t < first_lo)) {
+          if (j == 0) cv = info.y ? (float)((int)max(info.y, 7u) - 127) : 0.f;
+          ks *= exp2i(e0 == 255 ? 0 : max(e0, 7) - 127);
+          ve = (float)(e1 == 255 ? 0 : max(e1, 7) - 127);
+          pe = exp2i(min(max((int)(cv - ve), -126), 126));
+        }
+        if (masked && go && (!live || t < first_lo)) {
           // no row's key: the weights' zeros must not meet what the pool
           // holds there, or what shared memory held before
           unsigned char* v = sm + S::off_V + (size_t)(c % VS) * S::kTile;
@@ -335,7 +372,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
           float v[CH];
           load_cols(st + n0, v);
 #pragma unroll
-          for (int n = 0; n < CH; ++n) y[n0 + n] = v[n] * ks;
+          for (int n = 0; n < CH; ++n) y[n0 + n] = Q8 ? fmaf(v[n], ks * qe[n0 + n], ve) : v[n] * ks;
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -404,10 +441,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
           const float mr[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]));
-            l[n + q] += p;
-            const float x = Q8 ? (masked && y[n + q] == -INFINITY ? 0.f : p * vs) : p;
-            *reinterpret_cast<__nv_bfloat16*>(P + (n + q) * 128 + ((ch ^ ((n + q) & 7)) << 4)) = __float2bfloat16_rn(x);
+            const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]) + (Q8 ? kUp : 0.f));
+            l[n + q] = fmaf(p, pe, l[n + q]);
+            *reinterpret_cast<uint16_t*>(P + (n + q) * 128 + ((ch ^ ((n + q) & 7)) << 4)) =
+                Q8 ? (uint16_t)pack_f16x2(p, 0.f) : (uint16_t)pack_bf16x2(p, 0.f);
           }
         }
         tc::fence_proxy_async();
@@ -430,6 +467,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
       }
       const bool whole = w.whole();
       const int64_t at = (int64_t)w.slot(blockIdx.x) * RQ;
+      // 8-bit: O^T is in units of 2^(m - kUp), the sums of 2^(m - kUp - cv)
+      const float up = Q8 ? exp2i((int)cv) : 1.f, dm = Q8 ? kUp + cv : 0.f;
 #pragma unroll 1
       for (int n0 = 0; n0 < RQ; n0 += 8) {
         float o[8];
@@ -444,11 +483,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
               const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
               if (r < D)
                 (static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh)[r] =
-                    __float2bfloat16_rn(o[n] * inv);
-              if (r == 0 && a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m_s[row] + log2f(sum)) * 0.6931471805599453f;
+                    __float2bfloat16_rn(o[n] * up * inv);
+              if (r == 0 && a.lse)
+                a.lse[(w.s.r0 + tok) * a.Hq + head] = (m_s[row] - dm + log2f(sum)) * 0.6931471805599453f;
             } else {
-              if (r < D) a.part[(at + row) * D + r] = o[n];
-              if (r == 0) a.ml[at + row] = make_float2(m_s[row], sum);
+              if (r < D) a.part[(at + row) * D + r] = o[n] * up;
+              if (r == 0) a.ml[at + row] = make_float2(m_s[row] - dm, sum);
             }
           }
         }

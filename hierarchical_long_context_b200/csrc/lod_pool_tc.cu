@@ -14,20 +14,23 @@ template <int D, bool Q8>
 struct RowsSmem {
   static constexpr int kTile = 128 * D * 2;  // a K, V or Q tile
   static constexpr int kStages = D == 128 ? (Q8 ? 4 : 5) : 8;
-  static constexpr int kRaw = Q8 ? 128 * D + 128 : 0;  // codes and exponent bytes of a tile
+  static constexpr int kRaw = Q8 ? 128 * D + 256 : 0;  // codes and row factors of a tile
   static constexpr size_t off_Q = 0;                   // two query tiles
   static constexpr size_t off_KV = off_Q + 2 * kTile;  // ring: K, V of a key tile take turns
   static constexpr size_t off_raw = off_KV + (size_t)kStages * kTile;
   static constexpr size_t off_bar = off_raw + 2 * kRaw;
   static constexpr int kBars = 2 * kStages + 4 + 8 + 1;
-  static constexpr size_t off_wb = off_bar + 8 * kBars + 8;  // (only counted when the list is laid out here)
-  static constexpr size_t bytes = off_wb + 16 + 1024;
+  static constexpr size_t off_info = off_bar + 8 * kBars + 8;  // int [2][16] a tile's largest exponents
+  static constexpr size_t bytes = off_info + 128 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Roles: warp 0 TMA copies, warp 1 MMA issue (warps 2 and 3 idle); warps 4-7
-// and 8-11 the softmax of query tiles 0 and 1 (a thread per row); with an
-// 8-bit pool warps 12-15 turn codes into bf16 tiles.
+// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue (warp 3
+// idle); warps 4-7 and 8-11 the softmax of query tiles 0 and 1 (a thread per
+// row); with an 8-bit pool warps 12-15 turn codes into f16 tiles.  Such a
+// tile's rows are taken relative to its largest exponent, C: the keys' 2^C
+// joins the softmax scale, the values' joins the weights' exponent, and O_s
+// is kept in units of a running largest C.
 //
 // Tensor memory: S_0, S_1 (fp32, 128 columns each; the weights P_s, bf16
 // pairs, overwrite the first half of S_s), O_0, O_1.  The MMA warp issues,
@@ -44,6 +47,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   constexpr int NS = S::kStages;
   constexpr int kThreads = Q8 ? 512 : 384;
   constexpr float kTau = 8.f;
+  constexpr float kUp = 6.f;  // 8-bit: weights are up to 2^15 of f16's 2^16
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -58,6 +62,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   uint64_t* fin = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* info_s = reinterpret_cast<int*>(sm + S::off_info);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -65,7 +70,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       mbar_init(&full[i], Q8 ? 4 : 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i) {  // (keys', values')
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
       mbar_init(&s_full[i], 1);
@@ -95,65 +100,71 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 
   if (warp < 4) {
     regs_dec<40>();
-    if (warp == 0) {
-      // ============================================================ copies
-      Walk<kTM, kKT> w(a, a.Wb, blockIdx.x);
-      int c = 0;  // tiles copied (K and V count apart)
+    if (warp == 0 || warp == 2) {
+      // ============================================================ copies of keys, of values
+      const int kv = warp >> 1;
+      int t = 0;  // key tiles; the ring takes their keys and values in turn
       bool go = true;
-      for (; w.more() && go; w.next()) {
+      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
         Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
-        for (int kt = w.kt0; kt < w.kt1 && go; f.advance(kt), ++kt) {
-          const int mine = f.cur;
-          const unsigned ok = __ballot_sync(0xffffffffu, mine >= 0);
+        for (int kt = w.kt0; kt < w.kt1; f.advance(kt), ++kt, ++t) {
+          const unsigned ok = __ballot_sync(0xffffffffu, f.cur >= 0);
           const int rows = __popc(ok) << shift;
-          const int64_t row = ((int64_t)mine * a.pool.Hkv + w.u.h) << shift;
+          const int64_t row = ((int64_t)f.cur * a.pool.Hkv + w.u.h) << shift;
+          if constexpr (Q8) {
+            if (t >= 1 && !(go = wait(&raw_empty[kv], (uint32_t)(t - 1) & 1u))) break;
+            unsigned char* dst = sm + S::off_raw + kv * S::kRaw;
+            const int top = __shfl_sync(0xffffffffu, f.largest(), 8 * kv);
+            if (lane >> 3 == kv) {  // 16 rows' factors
+              const uint32_t e[4] = {f.ex.x, f.ex.y, f.ex.z, f.ex.w};
+              uint32_t x[8];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++c) {
-            if constexpr (Q8) {
-              const int st = c & 1;
-              if (c >= 2 && !(go = wait(&raw_empty[st], (uint32_t)((c - 2) >> 1) & 1u))) break;
-              unsigned char* dst = sm + S::off_raw + st * S::kRaw;
-              if (lane < 16 && (lane >> 3) == kv) *reinterpret_cast<uint4*>(dst + 128 * D + (lane & 7) * 16) = f.ex;
-              __syncwarp();
-              if (lane == 0) {
-                if (rows) mbar_arrive_expect(&raw_full[st], (uint32_t)rows * D);
-                else mbar_arrive(&raw_full[st]);
-              }
-              __syncwarp();
-              if (mine >= 0) {
-                const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-                bulk_g2s(dst + (lane << shift) * D, codes + row * D, (uint32_t)D << shift, &raw_full[st]);
-              }
-            } else {
-              const int st = c % NS;
-              if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
-              unsigned char* dst = sm + S::off_KV + (size_t)st * S::kTile;
-              if (lane == 0) {
-                if (rows) mbar_arrive_expect(&full[st], (uint32_t)rows * D * 2);
-                else mbar_arrive(&full[st]);
-              }
-              __syncwarp();
-              if (mine >= 0) {
-                const CUtensorMap* map = kv ? &maps.V : &maps.K;
-                unsigned char* d = dst + (lane << shift) * 128;
-                tma_load_box(d, map, 0, (int)row, &full[st]);
-                if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, &full[st]);
-              }
+              for (int i = 0; i < 8; ++i)
+                x[i] = row_factor((e[i >> 1] >> (16 * (i & 1))) & 0xff, top) |
+                       row_factor((e[i >> 1] >> (16 * (i & 1) + 8)) & 0xff, top) << 16;
+              uint4* fac = reinterpret_cast<uint4*>(dst + 128 * D) + 2 * (lane & 7);
+              fac[0] = make_uint4(x[0], x[1], x[2], x[3]);
+              fac[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+            if (lane == 0) info_s[kv * 16 + (t & 15)] = top;
+            __syncwarp();
+            if (lane == 0) {
+              if (rows) mbar_arrive_expect(&raw_full[kv], (uint32_t)rows * D);
+              else mbar_arrive(&raw_full[kv]);
+            }
+            __syncwarp();
+            if (f.cur >= 0)
+              bulk_g2s(dst + (lane << shift) * D, static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K) + row * D,
+                       (uint32_t)D << shift, &raw_full[kv]);
+          } else {
+            const int c = 2 * t + kv, st = c % NS;
+            if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
+            unsigned char* d = sm + S::off_KV + (size_t)st * S::kTile + (lane << shift) * 128;
+            if (lane == 0) {
+              if (rows) mbar_arrive_expect(&full[st], (uint32_t)rows * D * 2);
+              else mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (f.cur >= 0) {
+              const CUtensorMap* map = kv ? &maps.V : &maps.K;
+              tma_load_box(d, map, 0, (int)row, &full[st]);
+              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, &full[st]);
             }
           }
         }
       }
       __syncwarp();
       if (*abort_s && lane == 0) {  // copies still in flight land before the CTA ends
-        const int n = Q8 ? 2 : NS;
-        for (int i = c - 1; i >= 0 && i >= c - n; --i)
-          (void)mbar_wait(Q8 ? &raw_full[i % n] : &full[i % n], (uint32_t)(i / n) & 1u, a.status);
+        for (int i = t - 1; i >= 0 && i >= t - (Q8 ? 1 : NS); --i) {
+          const int c = 2 * i + kv;
+          (void)mbar_wait(Q8 ? &raw_full[kv] : &full[c % NS], (uint32_t)(Q8 ? i : c / NS) & 1u, a.status);
+        }
       }
     } else if (warp == 1) {
       // ============================================================ MMA issue
       if (lane == 0) {
-        const uint32_t idS = tc::idesc_bf16(128, 128, false, false);
-        const uint32_t idO = tc::idesc_bf16(128, D, false, true);
+        const uint32_t idS = Q8 ? idesc_f16(128, 128, false, false) : tc::idesc_bf16(128, 128, false, false);
+        const uint32_t idO = Q8 ? idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
         const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
         Walk<kTM, kKT> w(a, a.Wb, blockIdx.x);
         int c = 0;                          // ring position of the next K tile (V follows it)
@@ -215,7 +226,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     const int r = tid & 127;
     const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tl + s * 128, to = tmem + tl + kColO + s * 128;
-    const float scl = a.scale_log2;
     unsigned char* Qs = sm + S::off_Q + s * S::kTile;
     uint32_t ns = 0, no = 0;  // scores and outputs taken
     int c = 0;                // ring position of the next key tile's K
@@ -232,12 +242,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const int tok = g / G, head = w.u.h * G + g % G;
       const int p0 = (int)(w.s.len - w.s.n);
       const int pos = p0 + tok;
+      float row_scale = a.scale_log2;
       {
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + tok) * a.qt + (int64_t)head * a.qh;
         uint4 x[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) x[i] = mine ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+        if (Q8) row_scale = a.scale_log2 * exp2i(query_f16<D>(x));
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(Qs + (i >> 3) * kHalfBytes + sw_off(r, i)) = x[i];
         tc::fence_proxy_async();
@@ -256,14 +268,34 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const int first = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;  // this row's keys
       const int first_hi = a.window > 0 && pos_hi - a.window + 1 > 0 ? (int)(pos_hi - a.window + 1) : 0;
 
+      // keys of no row of the unit's two tiles
+      const int u0 = p0 + (int)w.u.i * kTM / G;
+      const int first_unit = a.window > 0 && u0 - a.window + 1 > 0 ? (int)(u0 - a.window + 1) : 0;
+
       float m = -INFINITY, l = 0.f;
+      int cv = 0;  // (8-bit) O_s is in units of 2^(cv - 127 - kUp)
       for (int j = 0; j < T; ++j, c += 2) {
         const int k0 = (w.kt0 + j) * kKT;
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || unit_bad;
-        const bool ragged = k0 + 127 >= w.s.len || unit_bad;  // V rows that are no keys
-        go = __all_sync(0xffffffffu, wait(&s_full[s], ns++ & 1u));
+        const bool ragged = k0 + 127 >= w.s.len || k0 < first_unit || unit_bad;  // V rows that are no keys
+        // (8-bit: the values' wait makes the tile's exponents visible)
+        go = __all_sync(0xffffffffu, (!Q8 || wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u)) &&
+                                         wait(&s_full[s], ns++ & 1u));
         if (!go) break;
         tc::fence_after_sync();
+        float scl = row_scale;
+        int df = 0;      // (8-bit) this tile's value exponent above cv
+        float fv = 1.f;  // and the factor O_s takes for a new cv
+        if constexpr (Q8) {
+          const int ck = info_s[(c >> 1) & 15], e = max(info_s[16 + ((c >> 1) & 15)], 7);
+          scl *= exp2i(max(ck, 7) - 127);
+          if (j == 0) cv = e;
+          if (e > cv + 1) {
+            fv = exp2i(max(cv - e, -126));
+            cv = e;
+          }
+          df = max(e - cv, -60);
+        }
         float y[128];
         tc::tmem_ld32xN<4>(ts, y);
         if (masked) {
@@ -282,11 +314,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         }
         if (ragged) {
           // P's zeros must not meet what the pool holds behind the length or
-          // what shared memory held before: those V rows become zero
+          // before every row's window, or what shared memory held before:
+          // those V rows become zero
           go = __all_sync(0xffffffffu, wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u));
           if (!go) break;
           const int t = k0 + r, i = t >> shift;
-          if (t >= w.s.len || table[i] < 0 || table[i] >= a.pool.blocks) {
+          if (t >= w.s.len || t < first_unit || table[i] < 0 || table[i] >= a.pool.blocks) {
             unsigned char* v = sm + S::off_KV + (size_t)((c + 1) % NS) * S::kTile;
 #pragma unroll
             for (int q = 0; q < D / 8; ++q)
@@ -304,24 +337,25 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         top = fmaxf(max3(top, y[124], y[125]), fmaxf(y[126], y[127])) * scl;
         const bool need = top > m + kTau || j == 0;
-        if (__any_sync(0xffffffffu, need)) {
+        if (__any_sync(0xffffffffu, need || fv != 1.f)) {
           const float mn = need ? fmaxf(top, m) : m;
           const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
           m = mn;
           l *= f;
+          const float fo = f * fv;
           if (j > 0) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
               float o[32];
               tc::tmem_ld32(to + 32 * q, o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
+              for (int e = 0; e < 32; ++e) o[e] *= fo;
               tc::tmem_st32(to + 32 * q, o);
             }
           }
         }
         const float2 sc2 = make_float2(scl, scl);
-        const float mu = m == -INFINITY ? 0.f : m;
+        const float mu = (m == -INFINITY ? 0.f : m) - (Q8 ? (float)df + kUp : 0.f);
         const float2 mu2 = make_float2(-mu, -mu);
         float2 la[4];
 #pragma unroll
@@ -335,7 +369,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             t.x = ex2_approx(t.x);
             t.y = ex2_approx(t.y);
             la[e & 3] = fadd2(la[e & 3], t);
-            pw[e] = pack_bf16x2(t.x, t.y);
+            pw[e] = Q8 ? pack_f16x2(t.x, t.y) : pack_bf16x2(t.x, t.y);
           }
           tmem_st16(ts + 16 * q, pw);
         }
@@ -344,7 +378,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_ready[s]);
         const float2 l2 = fadd2(fadd2(la[0], la[1]), fadd2(la[2], la[3]));
-        l += l2.x + l2.y;
+        l += (l2.x + l2.y) * (Q8 ? exp2i(-df - (int)kUp) : 1.f);
       }
       if (!go) break;
       // ---- the rows' results
@@ -352,7 +386,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       if (!go) break;
       tc::fence_after_sync();
       const bool whole = w.whole();
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float unit = Q8 ? exp2i(cv - 127 - (int)kUp) : 1.f;
+      const float inv = l > 0.f || l != l ? unit / l : 0.f;
       const int64_t at = (int64_t)w.slot(blockIdx.x) * kTM + s * 128 + r;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh;
 #pragma unroll 1
@@ -370,7 +405,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             reinterpret_cast<float4*>(a.part + at * D)[8 * q + e] =
-                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                make_float4(o[4 * e] * unit, o[4 * e + 1] * unit, o[4 * e + 2] * unit, o[4 * e + 3] * unit);
         }
         __syncwarp();
       }
@@ -391,8 +426,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
                                          (c < NS || wait(&empty[c % NS], (uint32_t)(c / NS - 1) & 1u)));
         if (!go) break;
         const unsigned char* src = sm + S::off_raw + (c & 1) * S::kRaw;
-        unsigned char* dst = sm + S::off_KV + (size_t)(c % NS) * S::kTile;
-        convert_tile<D, true>(src, src + 128 * D, dst, tid & 127);
+        convert_tile<D, true>(src, reinterpret_cast<const uint16_t*>(src + 128 * D),
+                              sm + S::off_KV + (size_t)(c % NS) * S::kTile, tid & 127);
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) {

@@ -53,12 +53,23 @@ __device__ __forceinline__ void regs_dec() {
 __device__ __forceinline__ uint32_t sw_off(int row, int chunk16) {  // 16-byte chunk of a 128B-swizzled row
   return (uint32_t)(row * 128 + (((chunk16 & 7) ^ (row & 7)) << 4));
 }
-__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-
+// Two floats rounded (RNE) to f16 and packed, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Instruction descriptor, kind::f16 with f16 inputs and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return tc::idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));  // formats 0: f16
+}
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
@@ -86,15 +97,16 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
 
 // ---------------------------------------------------------------- block entries
 
-// The copying warp's view of a piece's key tiles: the blocks of the present
-// tile (lane i: the tile's block i, -1: none or bad) and, of an 8-bit pool,
-// its exponent bytes (lanes 0-7 of the keys, 8-15 of the values, 16 tokens
-// each), read one and two tiles ahead so that no copy waits for them.
-template <bool Q8>
+// A copying warp's view of a piece's key tiles: the blocks of the present
+// tile (lane i: the tile's block i, -1: none or bad) and, with EX (an 8-bit
+// pool), its exponent bytes (lanes 0-7 of the keys, 8-15 of the values, 16
+// tokens each; 0 for tokens that are no keys), read one and two tiles ahead
+// so that no copy waits for them.
+template <bool EX>
 struct Feed {
   const PoolAttendArgs& a;
   const int32_t* table;
-  int nblk, kt1, h, cur, nxt;
+  int len, nblk, kt1, h, cur, nxt;
   uint4 ex;
 
   __device__ __forceinline__ int entry(int kt) const {
@@ -106,57 +118,99 @@ struct Feed {
     set_status(a.status, LOD_ST_BAD_PAGE);
     return -1;
   }
-  __device__ __forceinline__ uint4 exponents() const {
+  __device__ __forceinline__ uint4 exponents(int kt) const {
     const int lane = threadIdx.x & 31, x = (lane & 7) * 16;
     const int b = __shfl_sync(0xffffffffu, cur, x >> a.pool.shift);
     if (lane >= 16 || b < 0) return make_uint4(0, 0, 0, 0);
     const uint8_t* e = (lane < 8 ? a.pool.Ke : a.pool.Ve) + (((int64_t)b * a.pool.Hkv + h) << a.pool.shift);
-    return *reinterpret_cast<const uint4*>(e + (x & ((1 << a.pool.shift) - 1)));
+    uint4 v = *reinterpret_cast<const uint4*>(e + (x & ((1 << a.pool.shift) - 1)));
+    const int n = len - (kt * kKT + x);  // tokens of the 16
+    if (n < 16) {
+      uint32_t* w = &v.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = n - 4 * i;
+        w[i] &= k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1;
+      }
+    }
+    return v;
   }
-  __device__ __forceinline__ Feed(const PoolAttendArgs& args, int b, int head, int64_t len, int kt0, int end)
-      : a(args), table(args.batch.table + (int64_t)b * args.batch.max_blocks),
-        nblk((int)((len + (1 << args.pool.shift) - 1) >> args.pool.shift)), kt1(end), h(head) {
+  __device__ __forceinline__ Feed(const PoolAttendArgs& args, int b, int head, int64_t n, int kt0, int end)
+      : a(args), table(args.batch.table + (int64_t)b * args.batch.max_blocks), len((int)n),
+        nblk((int)((n + (1 << args.pool.shift) - 1) >> args.pool.shift)), kt1(end), h(head) {
     cur = entry(kt0);
     nxt = entry(kt0 + 1);
-    if (Q8) ex = exponents();
+    if (EX) ex = exponents(kt0);
   }
   __device__ __forceinline__ void advance(int kt) {  // from tile kt to kt + 1
     cur = nxt;
     nxt = entry(kt + 2);
-    if (Q8) ex = exponents();
+    if (EX) ex = exponents(kt + 1);
+  }
+  // The largest exponent byte of the tile's keys (in lanes 0-7) and values
+  // (lanes 8-15); 255, a row of NaN, does not count.
+  __device__ __forceinline__ int largest() const {
+    uint32_t m = 0;
+    const uint32_t w[4] = {ex.x, ex.y, ex.z, ex.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu4(m, w[i] & ~__vcmpeq4(w[i], 0xffffffffu));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __vmaxu4(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = __vmaxu4(m, m >> 16);
+    return (int)(__vmaxu4(m, m >> 8) & 0xff);
   }
 };
 
-// ---------------------------------------------------------------- e4m3 -> bf16
+// ---------------------------------------------------------------- e4m3 -> f16
 
-// Four e4m3 codes as four bf16 (two words), times f.  Shifted into a bf16's
-// exponent and mantissa, a code's low seven bits read as the code's value
-// times 2^-120 (bias 127 against 7; a subnormal code becomes a subnormal
-// bf16), so a product by 2^120 gives the value, exactly.
-__device__ __forceinline__ void e4m3x4_bf16(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-  lo = hmul2_bf16(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), f);
-  hi = hmul2_bf16(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), f);
-}
-// 2^120 2^(E - 127) in two factors (it can leave bf16's range), each in both
-// halves of a word; E = 255: NaN.  The pool never holds E below 7; smaller
-// ones read as 7.
-__device__ __forceinline__ void e4m3_factors(int E, uint32_t& f1, uint32_t& f2) {
-  const int e = (E < 7 ? 7 : E) - 127, e1 = e < 7 ? e : 7;
-  const uint32_t a = (uint32_t)(e1 + 120 + 127) << 7, b = E == 255 ? 0x7fc0u : (uint32_t)(e - e1 + 127) << 7;
-  f1 = a | (a << 16);
-  f2 = b | (b << 16);
+// The MMAs of an 8-bit pool take f16 operands: every e4m3 value is an f16
+// value, the hardware converts a pair in one instruction (into bf16 it takes
+// five on the integer pipe, which measured 3.5 times as long), and f16 weights
+// carry three bits more than bf16 ones.  What f16 lacks is range, so powers
+// of two are taken out of every operand and put back in fp32: the queries'
+// rows are scaled to a largest value in [2^14, 2^15) (what that loses lies
+// 2^-39 below the row's largest), and the rows' exponents are handled as the
+// kernels say.
+
+// Factor 2^(E - C) of a row of exponent byte E in a tile whose largest is C,
+// as f16 bits (a row 2^24 below the tile's largest is dropped: that is below
+// the rounding of the fp32 sums it would enter).
+__device__ __forceinline__ uint32_t row_factor(int E, int C) {
+  const int d = E - C;
+  return E == 255 || d >= 0 ? 0x3c00u : d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
 }
 
-// A tile of 128 rows of codes (src, rows of D bytes; ex: their exponent
-// bytes) as a bf16 tile in the 128-byte-swizzled layout, by 128 threads
-// (t < 128).  SCALED: times the rows' powers of two; else the codes' values.
-// A thread converts 16 codes of every (128 / (D / 16))-th row, so its place in
-// the swizzle is the same for all of them.  With D = 128 a row's two halves
-// lie on the same banks: the second half's threads store their two chunks in
-// the other order.
+// Exponent e that brings a query row with the largest bf16 magnitude bits
+// `top` to [2^14, 2^15) when multiplied by 2^-e; 0 for a row of zeros, of an
+// infinity or NaN.
+__device__ __forceinline__ int query_exponent(uint32_t top) {
+  if (top == 0 || top >= 0x7f80u) return 0;
+  const int e = (int)(top >> 7) - 127 - 14;
+  return e < -126 ? -126 : e;
+}
+// A query row of D bf16 channels (D / 8 words) as f16 times 2^-e; returns e.
+template <int D>
+__device__ __forceinline__ int query_f16(uint4 (&x)[D / 8]) {
+  uint32_t* w = &x[0].x;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < D / 2; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  const int e = query_exponent(top);
+  const float f = exp2i(-e);
+#pragma unroll
+  for (int i = 0; i < D / 2; ++i)
+    w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+  return e;
+}
+
+// A tile of 128 rows of codes (src, rows of D bytes) as an f16 tile in the
+// 128-byte-swizzled layout, by 128 threads (t < 128); with SCALED times the
+// rows' factors (fac, f16 bits).  A thread converts 16 codes of every
+// (128 / (D / 16))-th row, so its place in the swizzle is the same for all of
+// them.  With D = 128 a row's two halves lie on the same banks: the second
+// half's threads store their two chunks in the other order.
 template <int D, bool SCALED>
-__device__ __forceinline__ void convert_tile(const unsigned char* src, const unsigned char* ex, unsigned char* dst, int t) {
+__device__ __forceinline__ void convert_tile(const unsigned char* src, const uint16_t* fac, unsigned char* dst, int t) {
   constexpr int CPR = D / 16, RPI = 128 / CPR, IT = 128 / RPI;
   const int row0 = t / CPR, ch = t % CPR;
   const bool swap = D == 128 && (ch & 4);
@@ -166,24 +220,26 @@ __device__ __forceinline__ void convert_tile(const unsigned char* src, const uns
 #pragma unroll
   for (int i0 = 0; i0 < IT; i0 += BATCH) {
     uint4 v[BATCH];
-    int E[BATCH];
+    uint32_t f[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       v[i] = *reinterpret_cast<const uint4*>(src + (t + 128 * (i0 + i)) * 16);
-      if (SCALED) E[i] = ex[row0 + RPI * (i0 + i)];
+      if (SCALED) f[i] = fac[row0 + RPI * (i0 + i)] * 0x10001u;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const uint32_t w[4] = {swap ? v[i].z : v[i].x, swap ? v[i].w : v[i].y, swap ? v[i].x : v[i].z,
                              swap ? v[i].y : v[i].w};
       uint32_t x[8];
-      uint32_t f1 = 0x7b807b80u, f2 = 0;
-      if (SCALED) e4m3_factors(E[i], f1, f2);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) e4m3x4_bf16(w[q], f1, x[2 * q], x[2 * q + 1]);
-      if (SCALED) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = hmul2_bf16(x[q], f2);
+      for (int q = 0; q < 4; ++q) {
+        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+            : "=r"(x[2 * q]), "=r"(x[2 * q + 1])
+            : "r"(w[q]));
+        if (SCALED) {
+          x[2 * q] = hmul2_f16(x[2 * q], f[i]);
+          x[2 * q + 1] = hmul2_f16(x[2 * q + 1], f[i]);
+        }
       }
       unsigned char* r = d + (i0 + i) * RPI * 128;
       *reinterpret_cast<uint4*>(r + o0) = make_uint4(x[0], x[1], x[2], x[3]);

@@ -117,7 +117,10 @@ def attend64(pool, table, lens, begin, q, window=0, scale=None, bad_keys=None):
             lse = torch.logsumexp(s, -1)
             p = torch.exp(s - torch.where(lse == -math.inf, torch.zeros_like(lse), lse)[:, None])
             z[r0:r1, h] = lse
+            fin = torch.isfinite(v)
+            v = torch.where(fin, v, torch.zeros_like(v))
             o[r0:r1, h] = p @ v
+            o[r0:r1, h] += torch.where(seen.double() @ (~fin).double() > 0, math.nan, 0.0)  # (0 * NaN is NaN: only what is seen)
             spread = p @ v.abs()
             ds = (d + 2) * 2.0 ** -24 * mag
             tz[r0:r1, h] = ds + 2.0 ** -20 + L * 2.0 ** -24 + 2.0 ** -23 * lse.abs().nan_to_num(0, 0, 0)

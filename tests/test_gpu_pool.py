@@ -442,6 +442,45 @@ def test_attend_of_an_8_bit_pool_is_that_of_its_read_back(n):
     close(lse8, lse.double(), 2 * tz, "lse")
 
 
+@pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 3, 70])
+def test_attend_rows_of_many_sizes(n, dtype, bits):
+    """Key and value rows of sizes 2^-8 to 2^6, queries 2^-10 and 2^10 at a matching scale, rows of zeros."""
+    g = gen(50)
+    lens = [700, 200]
+    pool, table = make_pool(g, lens, 32, 8, 2, 128, dtype, 0)
+    f = torch.exp2(torch.randint(-8, 7, (2, *pool.K.shape[:3], 1), generator=g, device="cuda").float())
+    f[:, :, :, 3] = 0
+    K, V = (pool.K.float().nan_to_num(0) * f[0].clamp(max=1)).to(dtype), (pool.V.float().nan_to_num(0) * f[1]).to(dtype)
+    if bits:
+        (kc, ke), (vc, ve) = pt.quantise64(K), pt.quantise64(V)
+        pool = api.Pool(kc, vc, ke, ve, Hq=8, dtype=dtype)
+    else:
+        pool = api.Pool(K, V, Hq=8, dtype=dtype)
+    for m in (2.0 ** -10, 1.0, 2.0 ** 10):
+        check_attend(pool, table, lens, [n, n], 51, qmul=m, scale=0.1 / m)
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 0), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 60])
+def test_nan_and_infinite_rows_reach_only_the_queries_that_see_them(n, dtype, bits):
+    """A sequence whose rows hold NaN and infinities, appended as such: its queries' outputs are NaN, the other
+    sequence's, a window that ends before those rows, and keys behind the length are not touched."""
+    g = gen(52)
+    lens = [400, 333]
+    pool, table = make_pool(g, lens, 16, 4, 2, 64, dtype, bits)
+    begin, batch = make_batch(table, lens, [400, 0])
+    k, v = randn(g, 400, 2, 64, dtype=dtype), randn(g, 400, 2, 64, dtype=dtype)
+    k[5, :, 3], v[9, 0, 2] = math.nan, math.inf
+    lod.lod_pool_append(pool, batch, k, v)
+    begin, batch, q, out, lse, _ = run_attend(pool, table, lens, [n, n], 53)
+    assert torch.isnan(out[:n].float()).all() and torch.isnan(lse[:n]).all()
+    o, z, to, tz = pt.attend64(pool, table, lens, begin, q)
+    close(out[n:], o[n:], to[n:], "out")
+    close(lse[n:], z[n:], tz[n:], "lse")
+    check_attend(pool, table, lens, [n, n], 54, window=250)
+
+
 @pytest.mark.parametrize("dtype, bits", [(BF, 0), (F32, 8)])
 def test_attend_strides_and_default_outputs(dtype, bits):
     lens, new = [200, 90], [1, 30]
