@@ -23,15 +23,16 @@ struct FewSmem {
   static constexpr size_t off_Q = off_P + 2 * kP;              // [2][D / 64 halves][NQ][128 B]
   static constexpr size_t off_raw = off_Q + 2 * kQ;
   static constexpr size_t off_ex = off_raw + (Q8 ? (size_t)RS * 2 * kRaw : 0);  // uint8 [16][2][128]
-  static constexpr size_t off_m = off_ex + (Q8 ? 16 * 256 : 0);                 // float [NQ]
-  static constexpr size_t off_red = off_m + 4 * 64;                             // float [4][64]
-  static constexpr size_t off_qe = off_red + 4 * 4 * 64;                        // float [16][NQ]
-  static constexpr size_t off_pos = off_qe + (Q8 ? 16 * 4 * NQ : 0);                       // int2 [64]
-  static constexpr size_t off_info = off_pos + 8 * 64;                          // uint2 [16]
+  static constexpr size_t off_m = off_ex + (Q8 ? 16 * 256 : 0);       // float [2][64]
+  static constexpr size_t off_red = off_m + 2 * 4 * 64;               // float [2][4][64]
+  static constexpr size_t off_fin = off_red + 2 * 4 * 4 * 64;         // float2 [64]
+  static constexpr size_t off_qe = off_fin + 8 * 64;                  // float [16][NQ]
+  static constexpr size_t off_pos = off_qe + (Q8 ? 16 * 4 * NQ : 0);  // int2 [2][64]
+  static constexpr size_t off_info = off_pos + 2 * 8 * 64;                          // uint2 [16]
   static constexpr size_t off_wb = off_info + 128;                               // int64 [kInlineSeqs + 1]
   static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 2;
   static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
-  static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;
+  static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;  // (tmem slot, abort flag, a scale)
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // block masks, exponent bytes and query scales are kept for 16 tiles (units
   // have one at least): the copies run at
@@ -53,12 +54,15 @@ struct FewSmem {
 // so what f16 drops lies 2^-30 below the largest weighted value.
 // Roles: warp 0 copies of keys, warp 1 the MMAs of S^T, warp 2 those of O^T
 // (two issuers: neither waits for the other's operands), warp 3 query tiles
-// and copies of values, warps 4-7 softmax, with an 8-bit pool warps 8-11 and 12-15 codes to bf16
-// (keys, values).
+// and copies of values, warps 4-7 and 8-11 the softmax of even and odd tiles,
+// each with maxima, sums and an O^T of its own (a tile's chain of waits,
+// loads, exponentials and stores measured 1600 to 3000 cycles, more than its
+// bytes take, so two chains run side by side and are joined at the unit's
+// end), with an 8-bit pool warps 12-15 codes to f16.
 // Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
 // HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
 template <int D, int RQ, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
+__global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
   using S = FewSmem<D, RQ, Q8>;
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
@@ -87,6 +91,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   int2* pos_s = reinterpret_cast<int2*>(sm + S::off_pos);
   uint2* info_s = reinterpret_cast<uint2*>(sm + S::off_info);  // blocks that are there, largest value exponent
   float* qe_s = reinterpret_cast<float*>(sm + S::off_qe);
+  float* up_s = reinterpret_cast<float*>(const_cast<int*>(abort_s) + 1);
   unsigned char* ex_s = sm + S::off_ex;
   int64_t* wb_s = reinterpret_cast<int64_t*>(sm + S::off_wb);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  constexpr uint32_t kColO = 128;  // S^T in columns [0, 64) and [64, 128)
+  constexpr uint32_t kColO = 128;  // S^T in columns [0, 64) and [64, 128), O^T of even and odd tiles behind them
 
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, abort_s, a.status); };
   // wait for use number `i` of a ring of n barriers
@@ -196,7 +201,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
       (void)mbar_wait(Q8 ? &raw_full[(i % n) * 2 + kv] : (kv ? vfull : kfull) + i % n, (uint32_t)(i / n) & 1u, a.status);
   };
 
-  if (Q8 && warp < 4) regs_dec<72>();
+  if (warp < 4) regs_dec<72>();
   if (warp == 0) {
     // ============================================================== keys
     int c = 0;
@@ -249,8 +254,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
           const uint64_t pd = tc::desc_kmajor_sw128(pb + (uint32_t)(c & 1) * S::kP);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16(tmem + kColO, vd + kk * (2048 >> 4), pd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idO,
-                         j > 0 || kk > 0);
+            tc::mma_bf16(tmem + kColO + (c & 1) * 64, vd + kk * (2048 >> 4),
+                         pd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idO, j > 1 || kk > 0);
           tc::mma_commit(&pv_done[c & 1]);
           tc::mma_commit(&vempty[c % VS]);
         }
@@ -306,143 +311,145 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
       go = copies(w, 1, c);
     }
     drain(1, c);
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ============================================================== softmax
-    if (Q8) regs_inc<248>();
-    const int r = tid & 127;  // key of the tile; channel of O^T
+    regs_inc<Q8 ? 168 : 216>();
+    const int half = (warp - 4) >> 2;  // this warpgroup takes the tiles of this parity
+    const int r = tid & 127;           // key of the tile; channel of O^T
     const int q4 = warp & 3;
     const uint32_t tl = (uint32_t)(32 * q4) << 16;
-    constexpr int CH = RQ < 16 ? 8 : 16;  // columns of a TMEM load
+    const uint32_t ts = tmem + tl + half * 64, to = tmem + tl + kColO + half * 64;
+    const int bar_or = 1 + 2 * half, bar_wg = 2 + 2 * half;  // named barriers of the warpgroup
+    constexpr int kBarBoth = 5;                              // and of the two
+    constexpr int CH = RQ < 16 ? 8 : 16;                     // columns of a TMEM load
     auto load_cols = [&](uint32_t at, float (&v)[CH]) {
       if constexpr (CH == 8) tc::tmem_ld8(at, v);
       else tc::tmem_ld16(at, v);
     };
-    int c = 0, k = 0;
+    float* mine_m = m_s + half * 64;
+    float* red = red_s + half * 256;
+    int2* pos = pos_s + half * 64;
+    int c0 = 0, k = 0;  // the unit's first tile, units
     bool go = true;
-    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more(); w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
       const float* qe = qe_s + (k & 15) * NQ;
-      float cv = 0.f;  // (8-bit) the unit's value exponent: sums of weights are in units of 2^cv
+      float cv = 0.f;  // (8-bit) a value exponent of the unit: sums of weights are in units of 2^cv
       const int p0 = (int)(w.s.len - w.s.n), g0 = (int)w.u.i * RQ;
       const int pos_lo = p0 + g0 / a.G, pos_hi = p0 + (g0 + w.nrow - 1) / a.G;
-      auto first_of = [&](int pos) { return a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0; };
+      auto first_of = [&](int p) { return a.window > 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0; };
       const int first_lo = first_of(pos_lo), first_hi = first_of(pos_hi);
-      bar_named_sync(2, 128);  // the last unit's readers are done
       if (r < RQ) {
-        const int pos = p0 + (g0 + (r < w.nrow ? r : w.nrow - 1)) / a.G;
-        pos_s[r] = make_int2(first_of(pos), pos);  // the row's keys
-        m_s[r] = -INFINITY;
+        const int p = p0 + (g0 + (r < w.nrow ? r : w.nrow - 1)) / a.G;
+        pos[r] = make_int2(first_of(p), p);  // the row's keys
+        mine_m[r] = -INFINITY;
       }
-      bar_named_sync(2, 128);
+      bar_named_sync(bar_wg, 128);
       float l[RQ];
 #pragma unroll
       for (int n = 0; n < RQ; ++n) l[n] = 0.f;
-      for (int j = 0; j < T; ++j, ++c) {
-        const int k0 = (w.kt0 + j) * kKT, t = k0 + r;
+      const int j0 = (c0 ^ half) & 1;  // this warpgroup's first tile of the unit
+      for (int j = j0; j < T; j += 2) {
+        const int c = c0 + j, k0 = (w.kt0 + j) * kKT, t = k0 + r;
         go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
                                          wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
         const uint2 info = info_s[c & 15];
         const uint32_t ok = info.x;
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
-        const bool live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
+        bool live = true;
         float ks = a.scale_log2, ve = 0.f, pe = 1.f;
         if constexpr (Q8) {
           // (rows of exponent 255 hold NaN codes: any factor will do)
           const int e0 = ex_s[(c & 15) * 256 + r], e1 = ex_s[(c & 15) * 256 + 128 + r];
-          if (j == 0) cv = info.y ? (float)((int)max(info.y, 7u) - 127) : 0.f;
+          if (j == j0) cv = info.y ? (float)((int)max(info.y, 7u) - 127) : 0.f;
           ks *= exp2i(e0 == 255 ? 0 : max(e0, 7) - 127);
           ve = (float)(e1 == 255 ? 0 : max(e1, 7) - 127);
           pe = exp2i(min(max((int)(cv - ve), -126), 126));
         }
-        if (masked && go && (!live || t < first_lo)) {
-          // no row's key: the weights' zeros must not meet what the pool
-          // holds there, or what shared memory held before
-          unsigned char* v = sm + S::off_V + (size_t)(c % VS) * S::kTile;
+        if (masked) {
+          live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
+          if (go && (!live || t < first_lo)) {
+            // no row's key: the weights' zeros must not meet what the pool
+            // holds there, or what shared memory held before
+            unsigned char* v = sm + S::off_V + (size_t)(c % VS) * S::kTile;
 #pragma unroll
-          for (int q = 0; q < D / 8; ++q)
-            *reinterpret_cast<uint4*>(v + (q >> 3) * kHalfBytes + sw_off(r, q)) = make_uint4(0, 0, 0, 0);
+            for (int q = 0; q < D / 8; ++q)
+              *reinterpret_cast<uint4*>(v + (q >> 3) * kHalfBytes + sw_off(r, q)) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         tc::fence_after_sync();
         float y[RQ];
-        const uint32_t st = tmem + tl + (c & 1) * 64;
 #pragma unroll
         for (int n0 = 0; n0 < RQ; n0 += CH) {
           float v[CH];
-          load_cols(st + n0, v);
+          load_cols(ts + n0, v);
 #pragma unroll
           for (int n = 0; n < CH; ++n) y[n0 + n] = Q8 ? fmaf(v[n], ks * qe[n0 + n], ve) : v[n] * ks;
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[c & 1]);
+        if (lane == 0) mbar_arrive(&s_free[half]);
         if (masked) {
 #pragma unroll
           for (int n = 0; n < RQ; ++n) {
-            const int2 fl = pos_s[n];
+            const int2 fl = pos[n];
             y[n] = live && t >= fl.x && t <= fl.y ? y[n] : -INFINITY;
           }
         }
-        bool grow = j == 0 || !go;
+        bool grow = j == j0 || !go;
 #pragma unroll
         for (int n = 0; n < RQ; n += 4) {
-          const float4 mr = *reinterpret_cast<const float4*>(m_s + n);
+          const float4 mr = *reinterpret_cast<const float4*>(mine_m + n);
           grow |= y[n] > mr.x + kTau || y[n + 1] > mr.y + kTau || y[n + 2] > mr.z + kTau || y[n + 3] > mr.w + kTau;
         }
-        if (bar_red_or(1, 128, grow)) {
-          go = !bar_red_or(1, 128, !go);
+        if (bar_red_or(bar_or, 128, grow)) {
+          go = !bar_red_or(bar_or, 128, !go);
           if (!go) break;
-          // new maxima: over the warp's keys, then over the four warps
+          // new maxima: over the warp's keys, then over the four warps (the
+          // sums of tile c - 2 are complete: waited for above)
 #pragma unroll
           for (int n = 0; n < RQ; ++n) {
             const float x = warp_max(y[n]);
-            if (lane == n % 32) red_s[q4 * 64 + n] = x;
+            if (lane == n % 32) red[q4 * 64 + n] = x;
           }
-          bar_named_sync(2, 128);
-          float f[RQ];
+          bar_named_sync(bar_wg, 128);
 #pragma unroll
-          for (int n = 0; n < RQ; ++n) {
-            const float x = fmaxf(fmaxf(red_s[n], red_s[64 + n]), fmaxf(red_s[128 + n], red_s[192 + n]));
-            const float m = m_s[n];
-            f[n] = x > m ? (m == -INFINITY ? 0.f : ex2_approx(m - x)) : 1.f;
-            l[n] *= f[n];
-          }
-          if (j > 0) {
-            go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 1));
-            if (go) {
-              tc::fence_after_sync();
+          for (int n0 = 0; n0 < RQ; n0 += 8) {
+            float f[8];
 #pragma unroll
-              for (int n0 = 0; n0 < RQ; n0 += 8) {
-                float o[8];
-                tc::tmem_ld8(tmem + tl + kColO + n0, o);
+            for (int n = 0; n < 8; ++n) {
+              const int q = n0 + n;
+              const float x = fmaxf(fmaxf(red[q], red[64 + q]), fmaxf(red[128 + q], red[192 + q]));
+              const float m = mine_m[q];
+              f[n] = x > m ? (m == -INFINITY ? 0.f : ex2_approx(m - x)) : 1.f;
+              l[q] *= f[n];
+            }
+            if (j > j0) {
+              float o[8];
+              tc::tmem_ld8(to + n0, o);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) o[n] *= f[n0 + n];
-                tc::tmem_st8(tmem + tl + kColO + n0, o);
-              }
+              for (int n = 0; n < 8; ++n) o[n] *= f[n];
+              tc::tmem_st8(to + n0, o);
             }
           }
-          bar_named_sync(2, 128);  // every thread has read m_s
-          if (r < RQ) {
-            const float x = fmaxf(fmaxf(red_s[r], red_s[64 + r]), fmaxf(red_s[128 + r], red_s[192 + r]));
-            m_s[r] = fmaxf(x, m_s[r]);
-          }
-          if (bar_red_or(1, 128, !go)) {
-            go = false;
-            break;
-          }
+          bar_named_sync(bar_wg, 128);  // every thread has read the old maxima
+          if (r < RQ)
+            mine_m[r] = fmaxf(fmaxf(fmaxf(red[r], red[64 + r]), fmaxf(red[128 + r], red[192 + r])), mine_m[r]);
+          bar_named_sync(bar_wg, 128);
         }
         // weights
-        unsigned char* P = sm + S::off_P + (size_t)(c & 1) * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
+        unsigned char* P = sm + S::off_P + (size_t)half * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
         const int ch = (r & 63) >> 3;
 #pragma unroll
         for (int n = 0; n < RQ; n += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(m_s + n);
+          const float4 m4 = *reinterpret_cast<const float4*>(mine_m + n);
           const float mr[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]) + (Q8 ? kUp : 0.f));
-            l[n + q] = fmaf(p, pe, l[n + q]);
+            l[n + q] = Q8 ? fmaf(p, pe, l[n + q]) : l[n + q] + p;
             *reinterpret_cast<uint16_t*>(P + (n + q) * 128 + ((ch ^ ((n + q) & 7)) << 4)) =
                 Q8 ? (uint16_t)pack_f16x2(p, 0.f) : (uint16_t)pack_bf16x2(p, 0.f);
           }
@@ -450,75 +457,93 @@ __global__ void __launch_bounds__(Q8 ? 512 : 256, 1)
         tc::fence_proxy_async();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[c & 1]);
+        if (lane == 0) mbar_arrive(&p_ready[half]);
       }
-      if (!go) break;
-      // ---- the unit's result, or this CTA's piece of it
-      go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c - 1));
+      // ---- the unit's result, or this CTA's piece of it: warpgroup 1 hands
+      // its maxima and sums over, warpgroup 0 joins both
+      const int mine = (T - j0 + 1) >> 1;  // this warpgroup's tiles
+      if (go && mine > 0) go = __all_sync(0xffffffffu, wait_ring(pv_done, 2, c0 + j0 + 2 * (mine - 1)));
       tc::fence_after_sync();
 #pragma unroll
       for (int n = 0; n < RQ; ++n) {
         const float x = warp_sum(l[n]);
-        if (lane == n % 32) red_s[q4 * 64 + n] = x;
+        if (lane == n % 32) red[q4 * 64 + n] = x;
       }
-      if (bar_red_or(1, 128, !go)) {
-        go = false;
-        break;
-      }
-      const bool whole = w.whole();
-      const int64_t at = (int64_t)w.slot(blockIdx.x) * RQ;
+      bar_named_sync(bar_wg, 128);
       // 8-bit: O^T is in units of 2^(m - kUp), the sums of 2^(m - kUp - cv)
-      const float up = Q8 ? exp2i((int)cv) : 1.f, dm = Q8 ? kUp + cv : 0.f;
+      const float dm = Q8 ? kUp + cv : 0.f;
+      float2* fin_s = reinterpret_cast<float2*>(sm + S::off_fin);
+      const float up = Q8 ? exp2i((int)cv) : 1.f;
+      if (half == 1) {
+        if (r < RQ)
+          fin_s[r] = make_float2(mine_m[r] - dm, (red[r] + red[64 + r]) + (red[128 + r] + red[192 + r]));
+        if (r == 0) up_s[0] = mine > 0 ? up : 0.f;
+      }
+      go = !bar_red_or(kBarBoth, 256, !go);
+      if (!go) break;
+      if (half == 0) {
+        const bool whole = w.whole();
+        const int64_t at = (int64_t)w.slot(blockIdx.x) * RQ;
+        const float up1 = up_s[0];
 #pragma unroll 1
-      for (int n0 = 0; n0 < RQ; n0 += 8) {
-        float o[8];
-        tc::tmem_ld8(tmem + tl + kColO + n0, o);
+        for (int n0 = 0; n0 < RQ; n0 += 8) {
+          float o[8], o1[8];
+          tc::tmem_ld8(to + n0, o);
+          tc::tmem_ld8(to + 64 + n0, o1);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int row = n0 + n;
-          if (row < w.nrow) {
-            const float sum = (red_s[row] + red_s[64 + row]) + (red_s[128 + row] + red_s[192 + row]);
-            const int g = g0 + row, tok = g / a.G, head = w.u.h * a.G + g % a.G;
-            if (whole) {
-              const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-              if (r < D)
-                (static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh)[r] =
-                    __float2bfloat16_rn(o[n] * up * inv);
-              if (r == 0 && a.lse)
-                a.lse[(w.s.r0 + tok) * a.Hq + head] = (m_s[row] - dm + log2f(sum)) * 0.6931471805599453f;
-            } else {
-              if (r < D) a.part[(at + row) * D + r] = o[n] * up;
-              if (r == 0) a.ml[at + row] = make_float2(m_s[row] - dm, sum);
+          for (int n = 0; n < 8; ++n) {
+            const int row = n0 + n;
+            if (row < w.nrow) {
+              const float2 f1 = fin_s[row];
+              const float m0 = mine_m[row] - dm, l0 = (red[row] + red[64 + row]) + (red[128 + row] + red[192 + row]);
+              const float m = fmaxf(m0, f1.x), ref = m == -INFINITY ? 0.f : m;
+              const float a0 = ex2_approx(m0 - ref), a1 = ex2_approx(f1.x - ref);
+              const float sum = fmaf(l0, a0, f1.y * a1);
+              // (a warpgroup without a tile has nothing in its O^T)
+              const float x = (mine > 0 ? o[n] * (up * a0) : 0.f) + (up1 != 0.f ? o1[n] * (up1 * a1) : 0.f);
+              const int g = g0 + row, tok = g / a.G, head = w.u.h * a.G + g % a.G;
+              if (whole) {
+                const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+                if (r < D)
+                  (static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh)[r] =
+                      __float2bfloat16_rn(x * inv);
+                if (r == 0 && a.lse)
+                  a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(sum)) * 0.6931471805599453f;
+              } else {
+                if (r < D) a.part[(at + row) * D + r] = x;
+                if (r == 0) a.ml[at + row] = make_float2(m, sum);
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
       tc::fence_before_sync();
+      bar_named_sync(kBarBoth, 256);  // both O^T, fin_s and up_s have been read
+      c0 += T;
     }
   } else if constexpr (Q8) {
-    // ============================================================== codes to bf16 tiles
-    regs_dec<96>();
+    // ============================================================== codes to f16 tiles
+    regs_dec<104>();
     int c = 0;
     bool go = true;
-    const int t = tid & 127, kv = (warp - 8) >> 2;
-    const int n = kv ? VS : KS;
-    uint64_t* full = kv ? vfull : kfull;
-    uint64_t* empty = kv ? vempty : kempty;
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
-      for (int j = 0; j < w.kt1 - w.kt0; ++j, ++c) {
-        const int raw = (c % RS) * 2 + kv;
-        go = __all_sync(0xffffffffu, wait(&raw_full[raw], (uint32_t)(c / RS) & 1u) &&
-                                         (c < n || wait(&empty[c % n], (uint32_t)(c / n - 1) & 1u)));
-        if (!go) break;
-        const unsigned char* src = sm + S::off_raw + raw * S::kRaw;
-        unsigned char* dst = sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile;
-        convert_tile<D, false>(src, nullptr, dst, t);  // (the softmax multiplies by the powers of two)
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&raw_empty[raw]);
-          mbar_arrive(&full[c % n]);
+      for (int j = 0; j < w.kt1 - w.kt0 && go; ++j, ++c) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = kv ? VS : KS, raw = (c % RS) * 2 + kv;
+          go = __all_sync(0xffffffffu, wait(&raw_full[raw], (uint32_t)(c / RS) & 1u) &&
+                                           (c < n || wait((kv ? vempty : kempty) + c % n, (uint32_t)(c / n - 1) & 1u)));
+          if (!go) break;
+          // (the rows' powers of two are left to the softmax)
+          convert_tile<D, false>(sm + S::off_raw + raw * S::kRaw, nullptr,
+                                 sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile, tid & 127);
+          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[raw]);
+            mbar_arrive((kv ? vfull : kfull) + c % n);
+          }
         }
       }
     }
@@ -533,12 +558,12 @@ template <int D, int RQ, bool Q8>
 cudaError_t launch_few(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
   using S = FewSmem<D, RQ, Q8>;
   cudaError_t e = set_smem_once<pool_few_kernel<D, RQ, Q8>>(S::bytes);
-  // 128 (72 + 248 + 96 + 96) = 512 * 128
-  if (e == cudaSuccess && Q8) e = check_registers<pool_few_kernel<D, RQ, Q8>>(128);
+  // 128 (72 + 216 + 216) = 384 * 168 and 128 (72 + 168 + 168 + 104) = 512 * 128
+  if (e == cudaSuccess) e = check_registers<pool_few_kernel<D, RQ, Q8>>(Q8 ? 128 : 168);
   if (e == cudaSuccess && a.planned) e = launch_plan<RQ, kKT>(a, st);
   if (e != cudaSuccess) return e;
   PoolMaps none = {};
-  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 512 : 256, S::bytes, st>>>(maps ? *maps : none, a);
+  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 512 : 384, S::bytes, st>>>(maps ? *maps : none, a);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, RQ, kKT>(a, st);
 }

@@ -78,6 +78,16 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
                : "memory");
   return done;
 }
+// The same, the thread set aside for up to about 10 us: a role that is ahead
+// of the others leaves them the issue slots.
+__device__ __forceinline__ bool mbar_try_long(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done)
+               : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+               : "memory");
+  return done;
+}
 // Bounded wait for phase `parity` of `bar`; false once a wait of the CTA has
 // given up (abort_s), which a wait of about a second does.  The flag is looked
 // at only when the phase is not complete yet: a role waits several times a
@@ -86,7 +96,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   if (mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
   while (!*abort_s) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try_long(bar, parity)) return true;
     if (clock64() - t0 > (2ll << 30)) {
       set_status(status, LOD_ST_TIMEOUT);
       *abort_s = 1;
