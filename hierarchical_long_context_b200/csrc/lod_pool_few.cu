@@ -15,7 +15,7 @@ struct FewSmem {
   static constexpr int KS = kWide * (Q8 ? 1 : RQ == 64 ? 2 : 3);
   static constexpr int VS = kWide * (Q8 ? (RQ == 64 ? 1 : 2) : RQ >= 32 ? 2 : 3);
   static constexpr int RS = kWide * (RQ >= 32 ? 2 : 3);  // stages of codes (K and V of a tile)
-  static constexpr int kRaw = 128 * D;
+  static constexpr int kRaw = 128 * D;  // codes of a tile
   static constexpr int kQ = NQ * D * 2, kP = NQ * 256;
   static constexpr size_t off_V = 0;  // (with d = 64 MMA 2 reads one tile past a V tile: K tiles follow)
   static constexpr size_t off_K = off_V + (size_t)VS * kTile;
@@ -28,11 +28,11 @@ struct FewSmem {
   static constexpr size_t off_fin = off_red + 2 * 4 * 4 * 64;         // float2 [64]
   static constexpr size_t off_qe = off_fin + 8 * 64;                  // float [16][NQ]
   static constexpr size_t off_pos = off_qe + (Q8 ? 16 * 4 * NQ : 0);  // int2 [2][64]
-  static constexpr size_t off_info = off_pos + 2 * 8 * 64;                          // uint2 [16]
-  static constexpr size_t off_wb = off_info + 128;                               // int64 [kInlineSeqs + 1]
+  static constexpr size_t off_info = off_pos + 2 * 8 * 64;                          // uint32 [16]
+  static constexpr size_t off_wb = off_info + 64;                               // int64 [kInlineSeqs + 1]
   static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 2;
   static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
-  static constexpr size_t bytes = off_bar + 8 * kBars + 16 + 1024;  // (tmem slot, abort flag, a scale)
+  static constexpr size_t bytes = off_bar + 8 * kBars + 48 + 1024;  // (TMEM slot, abort flag, scales)
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
   // block masks, exponent bytes and query scales are kept for 16 tiles (units
   // have one at least): the copies run at
@@ -58,11 +58,11 @@ struct FewSmem {
 // each with maxima, sums and an O^T of its own (a tile's chain of waits,
 // loads, exponentials and stores measured 1600 to 3000 cycles, more than its
 // bytes take, so two chains run side by side and are joined at the unit's
-// end), with an 8-bit pool warps 12-15 codes to f16.
+// end), with an 8-bit pool warps 12-15 and 16-19 codes to f16 (keys, values).
 // Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
 // HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
 template <int D, int RQ, bool Q8>
-__global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
+__global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
   using S = FewSmem<D, RQ, Q8>;
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
@@ -89,9 +89,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   float* m_s = reinterpret_cast<float*>(sm + S::off_m);
   float* red_s = reinterpret_cast<float*>(sm + S::off_red);
   int2* pos_s = reinterpret_cast<int2*>(sm + S::off_pos);
-  uint2* info_s = reinterpret_cast<uint2*>(sm + S::off_info);  // blocks that are there, largest value exponent
+  uint32_t* info_s = reinterpret_cast<uint32_t*>(sm + S::off_info);  // blocks that are there
   float* qe_s = reinterpret_cast<float*>(sm + S::off_qe);
   float* up_s = reinterpret_cast<float*>(const_cast<int*>(abort_s) + 1);
+  float* top_s = up_s + 1;  // [2][4]
   unsigned char* ex_s = sm + S::off_ex;
   int64_t* wb_s = reinterpret_cast<int64_t*>(sm + S::off_wb);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -149,44 +150,40 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   const uint32_t all_ok = (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1);
 
   // The copies of a unit's keys (kv = 0) or values (kv = 1); `c` counts key
-  // tiles.  The values' warp also leaves each tile's block mask and, of an
-  // 8-bit pool, the exponent bytes of keys and values, before it announces
-  // the copy: the softmax waits for that one.
+  // tiles.  The values' warp also leaves each tile's block mask before it
+  // announces the copy: the softmax waits for that one.  An 8-bit pool's
+  // exponent bytes go with the codes, to a ring of their own (the codes'
+  // stage is free again before the softmax has used them).
   auto copies = [&](const Walk<RQ, kKT>& w, int kv, int& c) -> bool {
-    Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
+    Feed f(a, w.u.b, w.s.len, w.kt0, w.kt1);
     const int n = Q8 ? RS : kv ? VS : KS;
-    for (int kt = w.kt0; kt < w.kt1; f.advance(kt), ++kt, ++c) {
+    const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
+    const uint8_t* exps = kv ? a.pool.Ve : a.pool.Ke;
+    const CUtensorMap* map = kv ? &maps.V : &maps.K;
+    const int Hkv = a.pool.Hkv, h = w.u.h;
+    for (int kt = w.kt0; kt < w.kt1; f.advance(), ++kt, ++c) {
       const unsigned ok = __ballot_sync(0xffffffffu, f.cur >= 0);
       const int rows = __popc(ok) << shift;
-      const int64_t row = ((int64_t)f.cur * a.pool.Hkv + w.u.h) << shift;
+      const int row = (f.cur * Hkv + h) << shift;  // (a pool has fewer than 2^31 rows)
       const int st = c % n;
       uint64_t* full = Q8 ? &raw_full[st * 2 + kv] : (kv ? vfull : kfull) + st;
       if (c >= n && !wait(Q8 ? &raw_empty[st * 2 + kv] : (kv ? vempty : kempty) + st, (uint32_t)(c / n - 1) & 1u))
         return false;
-      if (kv == 1) {
-        int top = 0;
-        if (Q8) {
-          if (lane < 16) *reinterpret_cast<uint4*>(ex_s + (c & 15) * 256 + lane * 16) = f.ex;
-          top = __shfl_sync(0xffffffffu, f.largest(), 8);
-        }
-        if (lane == 0) info_s[c & 15] = make_uint2(ok, (uint32_t)top);
-        __syncwarp();
-      }
       if (lane == 0) {
-        if (rows) mbar_arrive_expect(full, (uint32_t)rows * D * (Q8 ? 1 : 2));
+        if (kv == 1) info_s[c & 15] = ok;
+        if (rows) mbar_arrive_expect(full, (uint32_t)rows * (Q8 ? D + 1 : 2 * D));
         else mbar_arrive(full);
       }
       __syncwarp();
       if (f.cur >= 0) {
         if constexpr (Q8) {
-          unsigned char* dst = sm + S::off_raw + (st * 2 + kv) * S::kRaw;
-          bulk_g2s(dst + (lane << shift) * D, static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K) + row * D,
+          bulk_g2s(sm + S::off_raw + (st * 2 + kv) * S::kRaw + (lane << shift) * D, codes + (int64_t)row * D,
                    (uint32_t)D << shift, full);
+          bulk_g2s(ex_s + (c & 15) * 256 + kv * 128 + (lane << shift), exps + row, 1u << shift, full);
         } else {
-          const CUtensorMap* map = kv ? &maps.V : &maps.K;
           unsigned char* d = sm + (kv ? S::off_V : S::off_K) + (size_t)st * S::kTile + (lane << shift) * 128;
-          tma_load_box(d, map, 0, (int)row, full);
-          if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, full);
+          tma_load_box(d, map, 0, row, full);
+          if (D == 128) tma_load_box(d + kHalfBytes, map, 64, row, full);
         }
       }
     }
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     drain(1, c);
   } else if (warp < 12) {
     // ============================================================== softmax
-    regs_inc<Q8 ? 168 : 216>();
+    regs_inc<Q8 ? 136 : 216>();
     const int half = (warp - 4) >> 2;  // this warpgroup takes the tiles of this parity
     const int r = tid & 127;           // key of the tile; channel of O^T
     const int q4 = warp & 3;
@@ -354,18 +351,15 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
                                          wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
-        const uint2 info = info_s[c & 15];
-        const uint32_t ok = info.x;
+        const uint32_t ok = info_s[c & 15];
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
         bool live = true;
-        float ks = a.scale_log2, ve = 0.f, pe = 1.f;
+        float ks = a.scale_log2, ve = 0.f;
         if constexpr (Q8) {
           // (rows of exponent 255 hold NaN codes: any factor will do)
           const int e0 = ex_s[(c & 15) * 256 + r], e1 = ex_s[(c & 15) * 256 + 128 + r];
-          if (j == j0) cv = info.y ? (float)((int)max(info.y, 7u) - 127) : 0.f;
           ks *= exp2i(e0 == 255 ? 0 : max(e0, 7) - 127);
           ve = (float)(e1 == 255 ? 0 : max(e1, 7) - 127);
-          pe = exp2i(min(max((int)(cv - ve), -126), 126));
         }
         if (masked) {
           live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
@@ -414,7 +408,15 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             const float x = warp_max(y[n]);
             if (lane == n % 32) red[q4 * 64 + n] = x;
           }
+          if (Q8 && j == j0) {
+            const float x = warp_max(live ? ve : -INFINITY);
+            if (lane == 0) top_s[half * 4 + q4] = x;
+          }
           bar_named_sync(bar_wg, 128);
+          if (Q8 && j == j0) {
+            const float x = fmaxf(fmaxf(top_s[half * 4], top_s[half * 4 + 1]), fmaxf(top_s[half * 4 + 2], top_s[half * 4 + 3]));
+            cv = x == -INFINITY ? 0.f : x;
+          }
 #pragma unroll
           for (int n0 = 0; n0 < RQ; n0 += 8) {
             float f[8];
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           bar_named_sync(bar_wg, 128);
         }
         // weights
+        const float pe = exp2i(min(max((int)(cv - ve), -126), 126));
         unsigned char* P = sm + S::off_P + (size_t)half * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
         const int ch = (r & 63) >> 3;
 #pragma unroll
@@ -524,26 +527,26 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to f16 tiles
-    regs_dec<104>();
+    regs_dec<64>();
     int c = 0;
     bool go = true;
+    const int kv = (warp - 12) >> 2, n = kv ? VS : KS;
+    uint64_t* full = kv ? vfull : kfull;
+    uint64_t* empty = kv ? vempty : kempty;
+    unsigned char* ring = sm + (kv ? S::off_V : S::off_K);
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
-      for (int j = 0; j < w.kt1 - w.kt0 && go; ++j, ++c) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int n = kv ? VS : KS, raw = (c % RS) * 2 + kv;
-          go = __all_sync(0xffffffffu, wait(&raw_full[raw], (uint32_t)(c / RS) & 1u) &&
-                                           (c < n || wait((kv ? vempty : kempty) + c % n, (uint32_t)(c / n - 1) & 1u)));
-          if (!go) break;
-          // (the rows' powers of two are left to the softmax)
-          convert_tile<D, false>(sm + S::off_raw + raw * S::kRaw, nullptr,
-                                 sm + (kv ? S::off_V : S::off_K) + (size_t)(c % n) * S::kTile, tid & 127);
-          tc::fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&raw_empty[raw]);
-            mbar_arrive((kv ? vfull : kfull) + c % n);
-          }
+      for (int j = w.kt0; j < w.kt1; ++j, ++c) {
+        const int raw = (c % RS) * 2 + kv;
+        go = __all_sync(0xffffffffu, wait(&raw_full[raw], (uint32_t)(c / RS) & 1u) &&
+                                         (c < n || wait(&empty[c % n], (uint32_t)(c / n - 1) & 1u)));
+        if (!go) break;
+        // (the rows' powers of two are left to the softmax)
+        convert_tile<D, false>(sm + S::off_raw + raw * S::kRaw, nullptr, ring + (size_t)(c % n) * S::kTile, tid & 127);
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[raw]);
+          mbar_arrive(&full[c % n]);
         }
       }
     }
@@ -558,12 +561,12 @@ template <int D, int RQ, bool Q8>
 cudaError_t launch_few(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
   using S = FewSmem<D, RQ, Q8>;
   cudaError_t e = set_smem_once<pool_few_kernel<D, RQ, Q8>>(S::bytes);
-  // 128 (72 + 216 + 216) = 384 * 168 and 128 (72 + 168 + 168 + 104) = 512 * 128
-  if (e == cudaSuccess) e = check_registers<pool_few_kernel<D, RQ, Q8>>(Q8 ? 128 : 168);
+  // 128 (72 + 216 + 216) = 384 * 168 and 128 (72 + 136 + 136 + 64 + 64) < 640 * 96
+  if (e == cudaSuccess) e = check_registers<pool_few_kernel<D, RQ, Q8>>(Q8 ? 96 : 168);
   if (e == cudaSuccess && a.planned) e = launch_plan<RQ, kKT>(a, st);
   if (e != cudaSuccess) return e;
   PoolMaps none = {};
-  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 512 : 384, S::bytes, st>>>(maps ? *maps : none, a);
+  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 640 : 384, S::bytes, st>>>(maps ? *maps : none, a);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, RQ, kKT>(a, st);
 }

@@ -14,20 +14,20 @@ template <int D, bool Q8>
 struct RowsSmem {
   static constexpr int kTile = 128 * D * 2;  // a K, V or Q tile
   static constexpr int kStages = D == 128 ? (Q8 ? 4 : 5) : 8;
-  static constexpr int kRaw = Q8 ? 128 * D + 256 : 0;  // codes and row factors of a tile
+  static constexpr int kRaw = Q8 ? 128 * D + 128 + 256 : 0;  // codes, exponent bytes and row factors of a tile
   static constexpr size_t off_Q = 0;                   // two query tiles
   static constexpr size_t off_KV = off_Q + 2 * kTile;  // ring: K, V of a key tile take turns
   static constexpr size_t off_raw = off_KV + (size_t)kStages * kTile;
   static constexpr size_t off_bar = off_raw + 2 * kRaw;
-  static constexpr int kBars = 2 * kStages + 4 + 8 + 1;
-  static constexpr size_t off_info = off_bar + 8 * kBars + 8;  // int [2][16] a tile's largest exponents
-  static constexpr size_t bytes = off_info + 128 + 1024;
+  static constexpr int kBars = 2 * kStages + 6 + 8 + 1;
+  static constexpr size_t off_info = off_bar + 8 * kBars + 8;  // int [2][16] a tile's largest exponents, [2][16] its blocks
+  static constexpr size_t bytes = off_info + 256 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue (warp 3
-// idle); warps 4-7 and 8-11 the softmax of query tiles 0 and 1 (a thread per
-// row); with an 8-bit pool warps 12-15 turn codes into f16 tiles.  Such a
+// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue; warps 4-7 and 8-11 the softmax of query tiles 0 and 1 (a thread per
+// row); with an 8-bit pool warps 12-15 turn codes into f16 tiles and warp 3
+// their exponents into factors.  Such a
 // tile's rows are taken relative to its largest exponent, C: the keys' 2^C
 // joins the softmax scale, the values' joins the weights' exponent, and O_s
 // is kept in units of a running largest C.
@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   uint64_t* empty = full + NS;
   uint64_t* raw_full = empty + NS;
   uint64_t* raw_empty = raw_full + 2;
-  uint64_t* s_full = raw_empty + 2;
+  uint64_t* fac_full = raw_empty + 2;
+  uint64_t* s_full = fac_full + 2;
   uint64_t* p_ready = s_full + 2;
   uint64_t* q_full = p_ready + 2;
   uint64_t* o_full = q_full + 2;
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     for (int i = 0; i < 2; ++i) {  // (keys', values')
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
+      mbar_init(&fac_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);
       mbar_init(&q_full[i], 4);
@@ -106,36 +108,27 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       int t = 0;  // key tiles; the ring takes their keys and values in turn
       bool go = true;
       for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
-        Feed<Q8> f(a, w.u.b, w.u.h, w.s.len, w.kt0, w.kt1);
-        for (int kt = w.kt0; kt < w.kt1; f.advance(kt), ++kt, ++t) {
+        Feed f(a, w.u.b, w.s.len, w.kt0, w.kt1);
+        const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
+        const uint8_t* exps = kv ? a.pool.Ve : a.pool.Ke;
+        const int Hkv = a.pool.Hkv, h = w.u.h;
+        for (int kt = w.kt0; kt < w.kt1; f.advance(), ++kt, ++t) {
           const unsigned ok = __ballot_sync(0xffffffffu, f.cur >= 0);
           const int rows = __popc(ok) << shift;
-          const int64_t row = ((int64_t)f.cur * a.pool.Hkv + w.u.h) << shift;
+          const int row = (f.cur * Hkv + h) << shift;  // (a pool has fewer than 2^31 rows)
           if constexpr (Q8) {
             if (t >= 1 && !(go = wait(&raw_empty[kv], (uint32_t)(t - 1) & 1u))) break;
             unsigned char* dst = sm + S::off_raw + kv * S::kRaw;
-            const int top = __shfl_sync(0xffffffffu, f.largest(), 8 * kv);
-            if (lane >> 3 == kv) {  // 16 rows' factors
-              const uint32_t e[4] = {f.ex.x, f.ex.y, f.ex.z, f.ex.w};
-              uint32_t x[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                x[i] = row_factor((e[i >> 1] >> (16 * (i & 1))) & 0xff, top) |
-                       row_factor((e[i >> 1] >> (16 * (i & 1) + 8)) & 0xff, top) << 16;
-              uint4* fac = reinterpret_cast<uint4*>(dst + 128 * D) + 2 * (lane & 7);
-              fac[0] = make_uint4(x[0], x[1], x[2], x[3]);
-              fac[1] = make_uint4(x[4], x[5], x[6], x[7]);
-            }
-            if (lane == 0) info_s[kv * 16 + (t & 15)] = top;
-            __syncwarp();
             if (lane == 0) {
-              if (rows) mbar_arrive_expect(&raw_full[kv], (uint32_t)rows * D);
+              info_s[32 + kv * 16 + (t & 15)] = (int)ok;
+              if (rows) mbar_arrive_expect(&raw_full[kv], (uint32_t)rows * (D + 1));
               else mbar_arrive(&raw_full[kv]);
             }
             __syncwarp();
-            if (f.cur >= 0)
-              bulk_g2s(dst + (lane << shift) * D, static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K) + row * D,
-                       (uint32_t)D << shift, &raw_full[kv]);
+            if (f.cur >= 0) {
+              bulk_g2s(dst + (lane << shift) * D, codes + (int64_t)row * D, (uint32_t)D << shift, &raw_full[kv]);
+              bulk_g2s(dst + 128 * D + (lane << shift), exps + row, 1u << shift, &raw_full[kv]);
+            }
           } else {
             const int c = 2 * t + kv, st = c % NS;
             if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
@@ -147,8 +140,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             __syncwarp();
             if (f.cur >= 0) {
               const CUtensorMap* map = kv ? &maps.V : &maps.K;
-              tma_load_box(d, map, 0, (int)row, &full[st]);
-              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, (int)row, &full[st]);
+              tma_load_box(d, map, 0, row, &full[st]);
+              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, row, &full[st]);
             }
           }
         }
@@ -218,6 +211,34 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         }
       }
       __syncwarp();
+    } else if (Q8) {
+      // ============================================================ row factors
+      int t = 0;
+      bool go = true;
+      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+        for (int kt = w.kt0; kt < w.kt1 && go; ++kt, ++t) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!(go = __all_sync(0xffffffffu, wait(&raw_full[kv], (uint32_t)t & 1u)))) break;
+            unsigned char* ex = sm + S::off_raw + kv * S::kRaw + 128 * D;
+            const uint32_t e4 = reinterpret_cast<const uint32_t*>(ex)[lane];
+            const int n = (int)w.s.len - kt * kKT - 4 * lane;  // tokens of this lane's four
+            const bool there = (info_s[32 + kv * 16 + (t & 15)] >> (4 * lane >> shift)) & 1;
+            uint32_t live = e4 & ~__vcmpeq4(e4, 0xffffffffu);  // (a row of NaN does not count)
+            live &= !there || n <= 0 ? 0u : n >= 4 ? 0xffffffffu : (1u << (8 * n)) - 1;
+            uint32_t m = __vmaxu4(live, live >> 16);
+            m = __vmaxu4(m, m >> 8) & 0xff;
+            const int top = (int)__reduce_max_sync(0xffffffffu, m);
+            uint32_t x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              x[i] = row_factor((e4 >> (16 * i)) & 0xff, top) | row_factor((e4 >> (16 * i + 8)) & 0xff, top) << 16;
+            reinterpret_cast<uint2*>(ex + 128)[lane] = make_uint2(x[0], x[1]);
+            if (lane == 0) info_s[kv * 16 + (t & 15)] = top;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fac_full[kv]);
+          }
+        }
+      }
     }
   } else if (warp < 12) {
     // ============================================================== softmax
@@ -422,11 +443,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     bool go = true;
     for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
       for (int x = 0; x < 2 * (w.kt1 - w.kt0); ++x, ++c) {
-        go = __all_sync(0xffffffffu, wait(&raw_full[c & 1], (uint32_t)(c >> 1) & 1u) &&
+        go = __all_sync(0xffffffffu, wait(&fac_full[c & 1], (uint32_t)(c >> 1) & 1u) &&
                                          (c < NS || wait(&empty[c % NS], (uint32_t)(c / NS - 1) & 1u)));
         if (!go) break;
         const unsigned char* src = sm + S::off_raw + (c & 1) * S::kRaw;
-        convert_tile<D, true>(src, reinterpret_cast<const uint16_t*>(src + 128 * D),
+        convert_tile<D, true>(src, reinterpret_cast<const uint16_t*>(src + 128 * D + 128),
                               sm + S::off_KV + (size_t)(c % NS) * S::kTile, tid & 127);
         tc::fence_proxy_async();
         __syncwarp();

@@ -108,66 +108,44 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
 // ---------------------------------------------------------------- block entries
 
 // A copying warp's view of a piece's key tiles: the blocks of the present
-// tile (lane i: the tile's block i, -1: none or bad) and, with EX (an 8-bit
-// pool), its exponent bytes (lanes 0-7 of the keys, 8-15 of the values, 16
-// tokens each; 0 for tokens that are no keys), read one and two tiles ahead
-// so that no copy waits for them.
-template <bool EX>
+// tile (lane i: the tile's block i, -1: none or bad).  A tile's copies take
+// less time to issue than a table entry takes to arrive, so entries are read
+// kAhead tiles ahead.
+constexpr int kAhead = 4;
 struct Feed {
   const PoolAttendArgs& a;
-  const int32_t* table;
-  int len, nblk, kt1, h, cur, nxt;
-  uint4 ex;
+  const int32_t* next;      // this lane's entry of the tile behind the queue
+  int left, per_tile, cur;  // left: entries of the sequence from `next` on
+  int tiles;                // tiles of the piece behind the queue
+  int ent[kAhead + 1];
 
-  __device__ __forceinline__ int entry(int kt) const {
-    const int per_tile = kKT >> a.pool.shift, lane = threadIdx.x & 31;
-    const int i = kt * per_tile + lane;
-    if (lane >= per_tile || i >= nblk || kt >= kt1) return -1;
-    const int e = table[i];
-    if (e >= 0 && e < a.pool.blocks) return e;
-    set_status(a.status, LOD_ST_BAD_PAGE);
-    return -1;
+  __device__ __forceinline__ int entry() {
+    const int lane = threadIdx.x & 31;
+    int e = INT32_MIN;
+    if (lane < per_tile && lane < left && tiles > 0) e = *next;
+    next += per_tile;
+    left -= per_tile;
+    --tiles;
+    return e;
   }
-  __device__ __forceinline__ uint4 exponents(int kt) const {
-    const int lane = threadIdx.x & 31, x = (lane & 7) * 16;
-    const int b = __shfl_sync(0xffffffffu, cur, x >> a.pool.shift);
-    if (lane >= 16 || b < 0) return make_uint4(0, 0, 0, 0);
-    const uint8_t* e = (lane < 8 ? a.pool.Ke : a.pool.Ve) + (((int64_t)b * a.pool.Hkv + h) << a.pool.shift);
-    uint4 v = *reinterpret_cast<const uint4*>(e + (x & ((1 << a.pool.shift) - 1)));
-    const int n = len - (kt * kKT + x);  // tokens of the 16
-    if (n < 16) {
-      uint32_t* w = &v.x;
+  __device__ __forceinline__ void present() {
+    cur = ent[0] >= 0 && ent[0] < a.pool.blocks ? ent[0] : -1;
+    if (ent[0] != INT32_MIN && cur < 0) set_status(a.status, LOD_ST_BAD_PAGE);
+  }
+  __device__ __forceinline__ Feed(const PoolAttendArgs& args, int b, int64_t len, int kt0, int kt1)
+      : a(args), per_tile(kKT >> args.pool.shift), tiles(kt1 - kt0) {
+    const int nblk = (int)((len + (1 << args.pool.shift) - 1) >> args.pool.shift);
+    next = args.batch.table + (int64_t)b * args.batch.max_blocks + (int64_t)kt0 * per_tile + (threadIdx.x & 31);
+    left = nblk - kt0 * per_tile;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = n - 4 * i;
-        w[i] &= k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1;
-      }
-    }
-    return v;
+    for (int i = 0; i <= kAhead; ++i) ent[i] = entry();
+    present();
   }
-  __device__ __forceinline__ Feed(const PoolAttendArgs& args, int b, int head, int64_t n, int kt0, int end)
-      : a(args), table(args.batch.table + (int64_t)b * args.batch.max_blocks), len((int)n),
-        nblk((int)((n + (1 << args.pool.shift) - 1) >> args.pool.shift)), kt1(end), h(head) {
-    cur = entry(kt0);
-    nxt = entry(kt0 + 1);
-    if (EX) ex = exponents(kt0);
-  }
-  __device__ __forceinline__ void advance(int kt) {  // from tile kt to kt + 1
-    cur = nxt;
-    nxt = entry(kt + 2);
-    if (EX) ex = exponents(kt + 1);
-  }
-  // The largest exponent byte of the tile's keys (in lanes 0-7) and values
-  // (lanes 8-15); 255, a row of NaN, does not count.
-  __device__ __forceinline__ int largest() const {
-    uint32_t m = 0;
-    const uint32_t w[4] = {ex.x, ex.y, ex.z, ex.w};
+  __device__ __forceinline__ void advance() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu4(m, w[i] & ~__vcmpeq4(w[i], 0xffffffffu));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = __vmaxu4(m, __shfl_xor_sync(0xffffffffu, m, o));
-    m = __vmaxu4(m, m >> 16);
-    return (int)(__vmaxu4(m, m >> 8) & 0xff);
+    for (int i = 0; i < kAhead; ++i) ent[i] = ent[i + 1];
+    ent[kAhead] = entry();
+    present();
   }
 };
 
