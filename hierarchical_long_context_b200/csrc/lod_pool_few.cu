@@ -11,10 +11,12 @@ struct FewSmem {
   static constexpr int NQ = RQ < 16 ? 16 : RQ;  // the MMAs' N (a multiple of 16 with M = 128)
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kWide = D == 64 ? 2 : 1;  // d = 64 has room for twice the stages
-  // stages: what 227 KB hold beside the query and weight tiles
-  static constexpr int KS = kWide * (Q8 ? 1 : RQ == 64 ? 2 : 3);
+  // stages: what 227 KB hold beside the query and weight tiles.  (8-bit, at
+  // most 16 rows: two bf16 tiles of each kind and two of codes, not one and
+  // three: with one the conversion of a tile waits for the MMAs of the last)
+  static constexpr int KS = kWide * (Q8 ? (RQ <= 16 ? 2 : 1) : RQ == 64 ? 2 : 3);
   static constexpr int VS = kWide * (Q8 ? (RQ == 64 ? 1 : 2) : RQ >= 32 ? 2 : 3);
-  static constexpr int RS = kWide * (RQ >= 32 ? 2 : 3);  // stages of codes (K and V of a tile)
+  static constexpr int RS = kWide * 2;  // stages of codes (K and V of a tile)
   static constexpr int kRaw = 128 * D;  // codes of a tile
   static constexpr int kQ = NQ * D * 2, kP = NQ * 256;
   static constexpr size_t off_V = 0;  // (with d = 64 MMA 2 reads one tile past a V tile: K tiles follow)
@@ -207,37 +209,39 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     drain(0, c);
   } else if (warp == 1) {
     // ============================================================== S^T = K Q^T
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_one();
       const uint32_t idS = Q8 ? idesc_f16(128, NQ, false, false) : tc::idesc_bf16(128, NQ, false, false);
       const uint32_t qb = smem_u32(sm + S::off_Q), kb = smem_u32(sm + S::off_K);
       int c = 0, k = 0;  // key tiles, units
       bool go = true;
       for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
-        if (!(go = wait_ring(q_full, 2, k))) break;
+        if (!(go = __all_sync(0xffffffffu, wait_ring(q_full, 2, k)))) break;
         const uint64_t qd = tc::desc_kmajor_sw128(qb + (uint32_t)(k & 1) * S::kQ);
         const int T = w.kt1 - w.kt0;
         for (int j = 0; j < T; ++j, ++c) {
-          if (!(go = (c < 2 || wait_ring(s_free, 2, c - 2)) && wait_ring(kfull, KS, c))) break;
+          if (!(go = __all_sync(0xffffffffu, (c < 2 || wait_ring(s_free, 2, c - 2)) && wait_ring(kfull, KS, c)))) break;
           tc::fence_after_sync();
           const uint64_t kd = tc::desc_kmajor_sw128(kb + (uint32_t)(c % KS) * S::kTile);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)  // (the address field of a descriptor counts 16 bytes)
-            tc::mma_bf16(tmem + (c & 1) * 64, kd + (((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4),
+            mma_ss(lead, tmem + (c & 1) * 64, kd + (((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4),
                          qd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idS, kk > 0);
-          tc::mma_commit(&s_full[c & 1]);
-          tc::mma_commit(&kempty[c % KS]);
-          if (j == T - 1) tc::mma_commit(&q_empty[k & 1]);
+          mma_commit_if(lead, &s_full[c & 1]);
+          mma_commit_if(lead, &kempty[c % KS]);
+          if (j == T - 1) mma_commit_if(lead, &q_empty[k & 1]);
         }
       }
       if (c > 0) {
-        tc::mma_commit(&fin[0]);
+        mma_commit_if(lead, &fin[0]);
         (void)mbar_wait(&fin[0], 0, a.status);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
     // ============================================================== O^T += V^T P^T
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_one();
       const uint32_t idO = Q8 ? idesc_f16(128, NQ, true, false) : tc::idesc_bf16(128, NQ, true, false);
       const uint32_t pb = smem_u32(sm + S::off_P), vb = smem_u32(sm + S::off_V);
       int c = 0;
@@ -245,20 +249,20 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next()) {
         const int T = w.kt1 - w.kt0;
         for (int j = 0; j < T; ++j, ++c) {
-          if (!(go = wait_ring(vfull, VS, c) && wait_ring(p_ready, 2, c))) break;
+          if (!(go = __all_sync(0xffffffffu, wait_ring(vfull, VS, c) && wait_ring(p_ready, 2, c)))) break;
           tc::fence_after_sync();
           const uint64_t vd = tc::desc_mnmajor_sw128(vb + (uint32_t)(c % VS) * S::kTile, kHalfBytes);
           const uint64_t pd = tc::desc_kmajor_sw128(pb + (uint32_t)(c & 1) * S::kP);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16(tmem + kColO + (c & 1) * 64, vd + kk * (2048 >> 4),
+            mma_ss(lead, tmem + kColO + (c & 1) * 64, vd + kk * (2048 >> 4),
                          pd + (((kk >> 2) * NQ * 128 + (kk & 3) * 32) >> 4), idO, j > 1 || kk > 0);
-          tc::mma_commit(&pv_done[c & 1]);
-          tc::mma_commit(&vempty[c % VS]);
+          mma_commit_if(lead, &pv_done[c & 1]);
+          mma_commit_if(lead, &vempty[c % VS]);
         }
       }
       if (c > 0) {
-        tc::mma_commit(&fin[1]);
+        mma_commit_if(lead, &fin[1]);
         (void)mbar_wait(&fin[1], 0, a.status);
       }
     }

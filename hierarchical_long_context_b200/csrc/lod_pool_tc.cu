@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       }
     } else if (warp == 1) {
       // ============================================================ MMA issue
-      if (lane == 0) {
+      {
+        const uint32_t lead = elect_one();
         const uint32_t idS = Q8 ? idesc_f16(128, 128, false, false) : tc::idesc_bf16(128, 128, false, false);
         const uint32_t idO = Q8 ? idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
         const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
@@ -163,50 +164,51 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         int c = 0;                          // ring position of the next K tile (V follows it)
         uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // weights and query tiles taken
         bool go = true, any = false;
-        auto full_wait = [&](int x) { return wait(&full[x % NS], (uint32_t)(x / NS) & 1u); };
+        auto uniform = [&](bool x) { return (bool)__all_sync(0xffffffffu, x); };
+        auto full_wait = [&](int x) { return uniform(wait(&full[x % NS], (uint32_t)(x / NS) & 1u)); };
         auto scores = [&](int s, int x) {  // S_s = Q_s K^T, K at ring position x
           const uint64_t qd = tc::desc_kmajor_sw128(qb + s * S::kTile);
           const uint64_t kd = tc::desc_kmajor_sw128(kvb + (uint32_t)(x % NS) * S::kTile);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // (the address field of a descriptor counts 16 bytes)
             const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-            tc::mma_bf16(tmem + s * 128, qd + o, kd + o, idS, kk > 0);
+            mma_ss(lead, tmem + s * 128, qd + o, kd + o, idS, kk > 0);
           }
-          tc::mma_commit(&s_full[s]);
+          mma_commit_if(lead, &s_full[s]);
           any = true;
         };
         for (; w.more() && go; w.next()) {
           const int tiles = w.nrow > 128 ? 2 : 1;
           const int T = w.kt1 - w.kt0;
-          for (int s = 0; s < tiles && go; ++s) go = wait(&q_full[s], nq[s]++ & 1u);
+          for (int s = 0; s < tiles && go; ++s) go = uniform(wait(&q_full[s], nq[s]++ & 1u));
           if (!go || !(go = full_wait(c))) break;
           tc::fence_after_sync();
           for (int s = 0; s < tiles; ++s) scores(s, c);
-          tc::mma_commit(&empty[c % NS]);
+          mma_commit_if(lead, &empty[c % NS]);
           for (int j = 0; j < T && go; ++j, c += 2) {
             for (int s = 0; s < tiles; ++s) {
-              if (!(go = wait(&p_ready[s], np[s]++ & 1u))) break;
+              if (!(go = uniform(wait(&p_ready[s], np[s]++ & 1u)))) break;
               if (s == 0 && !(go = full_wait(c + 1))) break;
               tc::fence_after_sync();
               const uint64_t vd = tc::desc_mnmajor_sw128(kvb + (uint32_t)((c + 1) % NS) * S::kTile, kHalfBytes);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc::mma_bf16_ts(tmem + kColO + s * 128, tmem + s * 128 + 8 * kk, vd + kk * (2048 >> 4), idO,
+                mma_ts(lead, tmem + kColO + s * 128, tmem + s * 128 + 8 * kk, vd + kk * (2048 >> 4), idO,
                                 j > 0 || kk > 0);
-              if (s == tiles - 1) tc::mma_commit(&empty[(c + 1) % NS]);
+              if (s == tiles - 1) mma_commit_if(lead, &empty[(c + 1) % NS]);
               if (j + 1 < T) {
                 if (s == 0 && !(go = full_wait(c + 2))) break;
                 tc::fence_after_sync();
                 scores(s, c + 2);
-                if (s == tiles - 1) tc::mma_commit(&empty[(c + 2) % NS]);
+                if (s == tiles - 1) mma_commit_if(lead, &empty[(c + 2) % NS]);
               } else {
-                tc::mma_commit(&o_full[s]);
+                mma_commit_if(lead, &o_full[s]);
               }
             }
           }
         }
         if (any) {
-          tc::mma_commit(fin);
+          mma_commit_if(lead, fin);
           (void)mbar_wait(fin, 0, a.status);
         }
       }
