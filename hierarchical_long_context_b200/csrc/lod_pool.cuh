@@ -73,7 +73,11 @@ struct ReadArgs {
 // TM query rows); row r of a sequence and KV head is query head r % G of its
 // new token r / G.  A unit's keys are cut into tiles of KT; the tiles of all
 // units, in the order sequence, head, row tile, key tile, are one list, and
-// CTA c takes the entries [c * share, (c + 1) * share) of it.
+// CTA c takes the entries [c * share, (c + 1) * share) of it.  Each unit opens
+// with kUnitCost entries that hold no tile: what a unit costs beside its tiles
+// (queries, first maxima, results).  Without them a CTA that gets a batch's
+// short sequences was the last to finish (150 us for 79 tiles, against 100).
+constexpr int kUnitCost = 3;
 struct PoolAttendArgs {
   const void* q;
   void* out;
@@ -131,8 +135,10 @@ __device__ __forceinline__ void row_tile_keys(const SeqView& s, int G, int64_t w
 struct Unit {
   int b, h;
   int64_t i;        // row tile
-  int64_t begin;    // list position of the unit's first key tile
-  int lo, hi;       // its key tiles [lo, hi); entry w is key tile lo + (w - begin)
+  int64_t begin;    // list position of the unit
+  int lo, hi;       // its key tiles [lo, hi); entry w is key tile lo + (w - first())
+  __device__ __forceinline__ int64_t first() const { return begin + kUnitCost; }
+  __device__ __forceinline__ int64_t end() const { return begin + kUnitCost + (hi - lo); }
 };
 
 template <int TM, int KT>
@@ -172,6 +178,7 @@ struct Walk {
   int64_t w0, w, w1, uend;
   Unit u;
   SeqView s;
+  int64_t pe;       // end of the piece
   int nt, kt0, kt1, nrow;
 
   __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* Wb, int cta) : a(args) {
@@ -185,38 +192,41 @@ struct Walk {
       s = seq_view(a.batch, a.pool.shift, u.b);
       nt = (s.n * a.G + TM - 1) / TM;
       piece();
+      if (kt0 == kt1) next();
     }
   }
   __device__ __forceinline__ bool more() const { return w < w1; }
   __device__ __forceinline__ void piece() {
-    uend = u.begin + (u.hi - u.lo);
-    const int64_t pe = uend < w1 ? uend : w1;
-    kt0 = u.lo + (int)(w - u.begin);
-    kt1 = u.lo + (int)(pe - u.begin);
+    uend = u.end();
+    pe = uend < w1 ? uend : w1;
+    kt0 = u.lo + (w > u.first() ? (int)(w - u.first()) : 0);
+    kt1 = u.lo + (pe > u.first() ? (int)(pe - u.first()) : 0);
     const int left = s.n * a.G - (int)u.i * TM;
     nrow = left < TM ? left : TM;
   }
   __device__ __forceinline__ void next() {
-    w += kt1 - kt0;
-    if (w >= w1) return;
-    u.begin = uend;  // a piece that does not reach its unit's end is the walk's last
-    if (u.i + 1 < nt) {
-      ++u.i;
-    } else {
-      u.i = 0;
-      if (++u.h == a.pool.Hkv) {
-        u.h = 0;
-        do {
-          s = seq_view(a.batch, a.pool.shift, ++u.b);
-        } while (s.n == 0);
-        nt = (s.n * a.G + TM - 1) / TM;
+    do {
+      w = pe;
+      if (w >= w1) return;
+      u.begin = uend;  // a piece that does not reach its unit's end is the walk's last
+      if (u.i + 1 < nt) {
+        ++u.i;
+      } else {
+        u.i = 0;
+        if (++u.h == a.pool.Hkv) {
+          u.h = 0;
+          do {
+            s = seq_view(a.batch, a.pool.shift, ++u.b);
+          } while (s.n == 0);
+          nt = (s.n * a.G + TM - 1) / TM;
+        }
       }
-    }
-    row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
-    piece();
+      row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
+      piece();
+    } while (kt0 == kt1);
   }
-  __device__ __forceinline__ bool whole() const { return w == u.begin && w + (kt1 - kt0) == uend; }
-  __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (u.begin >= w0 ? 1 : 0); }
+  __device__ __forceinline__ bool whole() const { return w <= u.first() && pe == uend; }
+  __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (u.first() >= w0 ? 1 : 0); }
 };
 
 // Sequences a CTA can lay out by itself (one row tile each): the list's
@@ -238,7 +248,7 @@ __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb
         if (s.n > 0) {
           int lo, hi;
           row_tile_keys<TM, KT>(s, a.G, a.window, 0, lo, hi);
-          n = (int64_t)(hi - lo) * a.pool.Hkv;
+          n = (int64_t)(hi - lo + kUnitCost) * a.pool.Hkv;
         }
       }
 #pragma unroll

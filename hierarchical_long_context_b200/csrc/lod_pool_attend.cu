@@ -36,17 +36,11 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
     Wb = wb_s;
   }
   clear_refused<T, D>(a);
-  const int64_t total = Wb[a.batch.B], share = list_share(a, total);
-  const int64_t w0 = blockIdx.x * share, w1 = w0 + share < total ? w0 + share : total;
-
-  for (int64_t w = w0; w < w1;) {
-    const Unit u = find_unit<TM, KT>(a, Wb, w);
-    const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
-    const int64_t uend = u.begin + (u.hi - u.lo);
-    const int64_t pe = uend < w1 ? uend : w1;
-    const int kt0 = u.lo + (int)(w - u.begin), kt1 = u.lo + (int)(pe - u.begin);
-    const int64_t row0 = u.i * TM, rows = (int64_t)s.n * a.G;
-    const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
+  for (Walk<TM, KT> w(a, Wb, blockIdx.x); w.more(); w.next()) {
+    const Unit& u = w.u;
+    const SeqView& s = w.s;
+    const int kt0 = w.kt0, kt1 = w.kt1, nrow = w.nrow;
+    const int64_t row0 = u.i * TM;
     const int32_t* table = a.batch.table + (int64_t)u.b * a.batch.max_blocks;
     const int64_t first_unit = a.window > 0 ? s.len - s.n + row0 / a.G - a.window + 1 : 0;  // (earlier keys: no row's)
 
@@ -199,8 +193,8 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
       }
     }
     // the unit's result, or this CTA's piece of it
-    const bool whole = w == u.begin && pe == uend;
-    const int slot = 2 * blockIdx.x + (u.begin >= w0 ? 1 : 0);
+    const bool whole = w.whole();
+    const int slot = w.slot(blockIdx.x);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = ty * RPT + i;
@@ -223,7 +217,6 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
         if (tx == 0) a.ml[(int64_t)slot * TM + r] = make_float2(m[i], l[i]);
       }
     }
-    w = pe;
   }
 }
 

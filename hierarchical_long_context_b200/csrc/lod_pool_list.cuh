@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
       if (i < nt) {
         int lo, hi;
         row_tile_keys<TM, KT>(s, a.G, a.window, i, lo, hi);
-        n = hi - lo;
+        n = hi - lo + kUnitCost;
       }
       int64_t v = n;
 #pragma unroll
@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
 
 // ---------------------------------------------------------------- merge
 
-// Joins the pieces of the unit that begins in CTA c's part of the list and
-// ends behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
+// Joins the pieces of the unit whose first tile lies in CTA c's part of the
+// list and whose last lies behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
 // in that order, so the result does not depend on which CTA ran when.  One
 // warp per row, blockIdx.y picks 16 rows.
 template <typename T, int D, int TM, int KT>
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
   const int64_t w0 = blockIdx.x * share, w1 = w0 + share;
   if (w1 >= total) return;
   const Unit u = find_unit<TM, KT>(a, Wb, w1 - 1);
-  const int64_t uend = u.begin + (u.hi - u.lo);
-  if (u.begin < w0 || uend <= w1) return;
+  const int64_t uend = u.end();
+  if (u.first() < w0 || u.first() >= w1 || uend <= w1) return;
   const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
   const int64_t rows = (int64_t)s.n * a.G, row0 = u.i * TM;
   const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
