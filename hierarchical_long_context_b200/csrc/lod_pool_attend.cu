@@ -243,7 +243,7 @@ cudaError_t launch_simt_d(const PoolAttendArgs& a, int TM, int bits, cudaStream_
 PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms) {
   PoolShape s = {};
   const int64_t rows = max_new * G;
-  s.kind = dtype != LOD_DTYPE_BF16 ? 0 : rows > 64 ? 1 : 2;
+  s.kind = dtype != LOD_DTYPE_BF16 ? 0 : rows > (bits == 8 ? 32 : 64) ? 1 : 2;
   if (s.kind == 2) {
     s.TM = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.KT = 128;

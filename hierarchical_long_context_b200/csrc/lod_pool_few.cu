@@ -1,5 +1,5 @@
 // lod_pool_few.cu -- exact attention of few new tokens (at most 64 query rows per
-// sequence and KV head) over the block pool: the cache streams past once.
+// sequence and KV head, 32 of an 8-bit pool) over the block pool: the cache streams past once.
 #include "lod_pool_list.cuh"
 #include "lod_pool_tc.cuh"
 
@@ -15,7 +15,7 @@ struct FewSmem {
   // most 16 rows: two bf16 tiles of each kind and two of codes, not one and
   // three: with one the conversion of a tile waits for the MMAs of the last)
   static constexpr int KS = kWide * (Q8 ? (RQ <= 16 ? 2 : 1) : RQ == 64 ? 2 : 3);
-  static constexpr int VS = kWide * (Q8 ? (RQ == 64 ? 1 : 2) : RQ >= 32 ? 2 : 3);
+  static constexpr int VS = kWide * (Q8 ? 2 : RQ >= 32 ? 2 : 3);
   static constexpr int RS = kWide * 2;  // stages of codes (K and V of a tile)
   static constexpr int kRaw = 128 * D;  // codes of a tile
   static constexpr int kQ = NQ * D * 2, kP = NQ * 256;
@@ -352,6 +352,9 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       const int j0 = (c0 ^ half) & 1;  // this warpgroup's first tile of the unit
       for (int j = j0; j < T; j += 2) {
         const int c = c0 + j, k0 = (w.kt0 + j) * kKT, t = k0 + r;
+        // (a barrier's parity tells a phase only from the one before it: with
+        // the sums of tile c - 2 complete, V_{c - VS} has landed)
+        static_assert(VS >= 2, "wait for the values");
         go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
                                          wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
@@ -581,7 +584,9 @@ cudaError_t launch_few_d(const PoolAttendArgs& a, const PoolMaps* maps, int TM, 
     case 8: return launch_few<D, 8, Q8>(a, maps, st);
     case 16: return launch_few<D, 16, Q8>(a, maps, st);
     case 32: return launch_few<D, 32, Q8>(a, maps, st);
-    default: return launch_few<D, 64, Q8>(a, maps, st);
+    default:
+      if constexpr (!Q8) return launch_few<D, 64, Q8>(a, maps, st);
+      return cudaErrorInvalidValue;  // (pool_shape gives more than 32 rows of an 8-bit pool to the other kernel)
   }
 }
 

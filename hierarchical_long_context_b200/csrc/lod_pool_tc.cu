@@ -19,33 +19,36 @@ struct RowsSmem {
   static constexpr size_t off_KV = off_Q + 2 * kTile;  // ring: K, V of a key tile take turns
   static constexpr size_t off_raw = off_KV + (size_t)kStages * kTile;
   static constexpr size_t off_bar = off_raw + 2 * kRaw;
-  static constexpr int kBars = 2 * kStages + 6 + 8 + 1;
+  static constexpr int kBars = 2 * kStages + 6 + 4 + 4 + 2 + 2 + 2 + 1;
   static constexpr size_t off_info = off_bar + 8 * kBars + 8;  // int [2][16] a tile's largest exponents, [2][16] its blocks
   static constexpr size_t bytes = off_info + 256 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue; warps 4-7 and 8-11 the softmax of query tiles 0 and 1 (a thread per
-// row); with an 8-bit pool warps 12-15 turn codes into f16 tiles and warp 3
-// their exponents into factors.  Such a
-// tile's rows are taken relative to its largest exponent, C: the keys' 2^C
+// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue; warps 4-7
+// and 8-11 the softmax of query tiles 0 and 1 (a thread per row); with an
+// 8-bit pool warps 12-15 turn codes into f16 tiles and warp 3 their exponents
+// into factors.  Such a tile's rows are taken relative to its largest exponent, C: the keys' 2^C
 // joins the softmax scale, the values' joins the weights' exponent, and O_s
 // is kept in units of a running largest C.
 //
 // Tensor memory: S_0, S_1 (fp32, 128 columns each; the weights P_s, bf16
-// pairs, overwrite the first half of S_s), O_0, O_1.  The MMA warp issues,
-// for each key tile j and query tile s in turn, O_s += P_s V_j and
-// S_s = Q_s K_{j+1}^T; while it works on one query tile the other tile's
-// softmax runs.  MMAs of one thread run in order, so S_s(j + 1) complete
-// means O_s(j) complete: the softmax warps may then rescale O_s themselves,
-// which they do only when a row's maximum has grown by more than 2^8
-// (weights up to 2^8 are as exact as any in bf16 and fp32).
+// pairs, overwrite the first half of each 64-column half of S_s), O_0, O_1.
+// Scores, weights and sums go by halves of 64 keys: for each half u the MMA
+// warp issues, for query tile s = 0, 1, O_s += P_s V_j (half u), then S_s =
+// Q_s K_{j+1}^T (half u), so a softmax warpgroup works on one half while the
+// MMAs of its other half run.  (With one buffer of 128 keys a warpgroup waited
+// 1550 of every 3650 cycles for its own MMAs.)
+// The softmax warps rescale O_s themselves, and only when a row's maximum has
+// grown by more than 2^8 (weights up to 2^8 are as exact as any in bf16 and
+// fp32).
+// Bounds, per 128 keys and 256 rows: 2048 cycles of tensor work (d = 128), 2048
+// of exponentials (16 a clock).
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     pool_rows_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
   using S = RowsSmem<D, Q8>;
   constexpr int NS = S::kStages;
-  constexpr int kThreads = Q8 ? 512 : 384;
   constexpr float kTau = 8.f;
   constexpr float kUp = 6.f;  // 8-bit: weights are up to 2^15 of f16's 2^16
   extern __shared__ unsigned char smem_raw[];
@@ -57,9 +60,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   uint64_t* raw_empty = raw_full + 2;
   uint64_t* fac_full = raw_empty + 2;
   uint64_t* s_full = fac_full + 2;
-  uint64_t* p_ready = s_full + 2;
-  uint64_t* q_full = p_ready + 2;
-  uint64_t* o_full = q_full + 2;
+  uint64_t* p_ready = s_full + 4;  // (of query tile and key half: [2][2])
+  uint64_t* q_full = p_ready + 4;
+  uint64_t* pv_done = q_full + 2;
+  uint64_t* o_full = pv_done + 2;
   uint64_t* fin = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -75,10 +79,13 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
       mbar_init(&fac_full[i], 1);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);
-      mbar_init(&q_full[i], 4);
-      mbar_init(&o_full[i], 1);
     }
     mbar_init(fin, 1);
     *abort_s = 0;
@@ -101,7 +108,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   const int per_tile = kKT >> shift;  // blocks of a key tile
 
   if (warp < 4) {
-    regs_dec<40>();
+    regs_dec<Q8 ? 80 : 104>();
     if (warp == 0 || warp == 2) {
       // ============================================================ copies of keys, of values
       const int kv = warp >> 1;
@@ -155,62 +162,68 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       }
     } else if (warp == 1) {
       // ============================================================ MMA issue
-      {
-        const uint32_t lead = elect_one();
-        const uint32_t idS = Q8 ? idesc_f16(128, 128, false, false) : tc::idesc_bf16(128, 128, false, false);
-        const uint32_t idO = Q8 ? idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
-        const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
-        Walk<kTM, kKT> w(a, a.Wb, blockIdx.x);
-        int c = 0;                          // ring position of the next K tile (V follows it)
-        uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // weights and query tiles taken
-        bool go = true, any = false;
-        auto uniform = [&](bool x) { return (bool)__all_sync(0xffffffffu, x); };
-        auto full_wait = [&](int x) { return uniform(wait(&full[x % NS], (uint32_t)(x / NS) & 1u)); };
-        auto scores = [&](int s, int x) {  // S_s = Q_s K^T, K at ring position x
-          const uint64_t qd = tc::desc_kmajor_sw128(qb + s * S::kTile);
-          const uint64_t kd = tc::desc_kmajor_sw128(kvb + (uint32_t)(x % NS) * S::kTile);
+      const uint32_t lead = elect_one();
+      const uint32_t idS = Q8 ? idesc_f16(128, 64, false, false) : tc::idesc_bf16(128, 64, false, false);
+      const uint32_t idO = Q8 ? idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
+      const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
+      int c = 0;                                // ring position of the next K tile (V follows it)
+      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // weights (of key tiles) and query tiles taken
+      bool go = true, any = false;
+      auto uniform = [&](bool x) { return (bool)__all_sync(0xffffffffu, x); };
+      auto full_wait = [&](int x) { return uniform(wait(&full[x % NS], (uint32_t)(x / NS) & 1u)); };
+      auto scores = [&](int s, int u, int x) {  // S_s, half u: Q_s K^T, K at ring position x
+        const uint64_t qd = tc::desc_kmajor_sw128(qb + s * S::kTile);
+        const uint64_t kd = tc::desc_kmajor_sw128(kvb + (uint32_t)(x % NS) * S::kTile + u * 64 * 128);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {  // (the address field of a descriptor counts 16 bytes)
-            const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-            mma_ss(lead, tmem + s * 128, qd + o, kd + o, idS, kk > 0);
-          }
-          mma_commit_if(lead, &s_full[s]);
-          any = true;
-        };
-        for (; w.more() && go; w.next()) {
-          const int tiles = w.nrow > 128 ? 2 : 1;
-          const int T = w.kt1 - w.kt0;
-          for (int s = 0; s < tiles && go; ++s) go = uniform(wait(&q_full[s], nq[s]++ & 1u));
-          if (!go || !(go = full_wait(c))) break;
-          tc::fence_after_sync();
-          for (int s = 0; s < tiles; ++s) scores(s, c);
-          mma_commit_if(lead, &empty[c % NS]);
-          for (int j = 0; j < T && go; ++j, c += 2) {
-            for (int s = 0; s < tiles; ++s) {
-              if (!(go = uniform(wait(&p_ready[s], np[s]++ & 1u)))) break;
-              if (s == 0 && !(go = full_wait(c + 1))) break;
+        for (int kk = 0; kk < D / 16; ++kk) {  // (the address field of a descriptor counts 16 bytes)
+          const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+          mma_ss(lead, tmem + s * 128 + u * 64, qd + o, kd + o, idS, kk > 0);
+        }
+        mma_commit_if(lead, &s_full[2 * s + u]);
+        any = true;
+      };
+      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+        const int tiles = w.nrow > 128 ? 2 : 1;
+        const int T = w.kt1 - w.kt0;
+        for (int s = 0; s < tiles && go; ++s) go = uniform(wait(&q_full[s], nq[s]++ & 1u));
+        if (!go || !(go = full_wait(c))) break;
+        tc::fence_after_sync();
+        for (int u = 0; u < 2; ++u)
+          for (int s = 0; s < tiles; ++s) scores(s, u, c);
+        mma_commit_if(lead, &empty[c % NS]);
+        for (int j = 0; j < T && go; ++j, c += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            for (int s = 0; s < tiles && go; ++s) {
+              go = uniform(wait(&p_ready[2 * s + u], np[s] & 1u)) && (u + s > 0 || full_wait(c + 1));
+              if (!go) break;
+              np[s] += u;
               tc::fence_after_sync();
               const uint64_t vd = tc::desc_mnmajor_sw128(kvb + (uint32_t)((c + 1) % NS) * S::kTile, kHalfBytes);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(lead, tmem + kColO + s * 128, tmem + s * 128 + 8 * kk, vd + kk * (2048 >> 4), idO,
-                                j > 0 || kk > 0);
-              if (s == tiles - 1) mma_commit_if(lead, &empty[(c + 1) % NS]);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(lead, tmem + kColO + s * 128, tmem + s * 128 + u * 64 + 8 * kk, vd + (4 * u + kk) * (2048 >> 4),
+                       idO, j > 0 || u + kk > 0);
+              mma_commit_if(lead, &pv_done[s]);
+              const bool last = u == 1 && s == tiles - 1;
+              if (last) mma_commit_if(lead, &empty[(c + 1) % NS]);
               if (j + 1 < T) {
-                if (s == 0 && !(go = full_wait(c + 2))) break;
-                tc::fence_after_sync();
-                scores(s, c + 2);
-                if (s == tiles - 1) mma_commit_if(lead, &empty[(c + 2) % NS]);
-              } else {
+                if (u + s == 0) {
+                  if (!(go = full_wait(c + 2))) break;
+                  tc::fence_after_sync();
+                }
+                scores(s, u, c + 2);
+                if (last) mma_commit_if(lead, &empty[(c + 2) % NS]);
+              } else if (u == 1) {
                 mma_commit_if(lead, &o_full[s]);
               }
             }
           }
         }
-        if (any) {
-          mma_commit_if(lead, fin);
-          (void)mbar_wait(fin, 0, a.status);
-        }
+      }
+      if (any) {
+        mma_commit_if(lead, fin);
+        (void)mbar_wait(fin, 0, a.status);
       }
       __syncwarp();
     } else if (Q8) {
@@ -244,13 +257,13 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     }
   } else if (warp < 12) {
     // ============================================================== softmax
-    regs_inc<Q8 ? 200 : 232>();
+    regs_inc<Q8 ? 176 : 200>();
     const int s = (warp - 4) >> 2;  // query tile
     const int r = tid & 127;
     const uint32_t tl = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + tl + s * 128, to = tmem + tl + kColO + s * 128;
     unsigned char* Qs = sm + S::off_Q + s * S::kTile;
-    uint32_t ns = 0, no = 0;  // scores and outputs taken
+    uint32_t ns = 0, no = 0;  // key halves and outputs taken
     int c = 0;                // ring position of the next key tile's K
     bool go = true;
     for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
@@ -297,18 +310,20 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 
       float m = -INFINITY, l = 0.f;
       int cv = 0;  // (8-bit) O_s is in units of 2^(cv - 127 - kUp)
-      for (int j = 0; j < T; ++j, c += 2) {
-        const int k0 = (w.kt0 + j) * kKT;
-        const bool masked = k0 + 127 > pos_lo || k0 < first_hi || unit_bad;
-        const bool ragged = k0 + 127 >= w.s.len || k0 < first_unit || unit_bad;  // V rows that are no keys
-        // (8-bit: the values' wait makes the tile's exponents visible)
-        go = __all_sync(0xffffffffu, (!Q8 || wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u)) &&
-                                         wait(&s_full[s], ns++ & 1u));
-        if (!go) break;
-        tc::fence_after_sync();
+      for (int j = 0; j < T && go; ++j, c += 2) {
+        const int kt = w.kt0 + j;
         float scl = row_scale;
         int df = 0;      // (8-bit) this tile's value exponent above cv
         float fv = 1.f;  // and the factor O_s takes for a new cv
+        const bool ragged = kt * kKT + 127 >= w.s.len || kt * kKT < first_unit || unit_bad;  // V rows that are no keys
+        if (Q8 || ragged) {
+          // The tile's values (8-bit: with them its exponents).  A barrier's
+          // parity tells a phase only from the one before it: the scores are
+          // waited for first, as with K_j every earlier copy has landed.
+          go = __all_sync(0xffffffffu, wait(&s_full[2 * s], (ns >> 1) & 1u) &&
+                                           wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u));
+          if (!go) break;
+        }
         if constexpr (Q8) {
           const int ck = info_s[(c >> 1) & 15], e = max(info_s[16 + ((c >> 1) & 15)], 7);
           scl *= exp2i(max(ck, 7) - 127);
@@ -319,29 +334,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           }
           df = max(e - cv, -60);
         }
-        float y[128];
-        tc::tmem_ld32xN<4>(ts, y);
-        if (masked) {
-          const int hi = pos - k0, lo = first - k0;
-#pragma unroll
-          for (int e = 0; e < 128; ++e) y[e] = e <= hi && e >= lo ? y[e] : -INFINITY;
-          if (unit_bad) {
-            for (int x = 0; x < per_tile; ++x) {
-              const int i = (w.kt0 + j) * per_tile + x;
-              if (i < nblk && table[i] >= 0 && table[i] < a.pool.blocks) continue;
-#pragma unroll
-              for (int e = 0; e < 128; ++e)
-                if (e >> shift == x) y[e] = -INFINITY;
-            }
-          }
-        }
         if (ragged) {
           // P's zeros must not meet what the pool holds behind the length or
           // before every row's window, or what shared memory held before:
           // those V rows become zero
-          go = __all_sync(0xffffffffu, wait(&full[(c + 1) % NS], (uint32_t)((c + 1) / NS) & 1u));
-          if (!go) break;
-          const int t = k0 + r, i = t >> shift;
+          const int t = kt * kKT + r, i = t >> shift;
           if (t >= w.s.len || t < first_unit || table[i] < 0 || table[i] >= a.pool.blocks) {
             unsigned char* v = sm + S::off_KV + (size_t)((c + 1) % NS) * S::kTile;
 #pragma unroll
@@ -351,57 +348,85 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           tc::fence_proxy_async();
           __syncwarp();
         }
-        float mx[4] = {y[0], y[1], y[2], y[3]};
-#pragma unroll
-        for (int e = 4; e < 124; e += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], y[e + q], y[e + 4 + q]);
-        }
-        float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        top = fmaxf(max3(top, y[124], y[125]), fmaxf(y[126], y[127])) * scl;
-        const bool need = top > m + kTau || j == 0;
-        if (__any_sync(0xffffffffu, need || fv != 1.f)) {
-          const float mn = need ? fmaxf(top, m) : m;
-          const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-          m = mn;
-          l *= f;
-          const float fo = f * fv;
-          if (j > 0) {
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              float o[32];
-              tc::tmem_ld32(to + 32 * q, o);
+        for (int u = 0; u < 2; ++u, ++ns) {
+          const int k0 = kt * kKT + u * 64;
+          const bool masked = k0 + 63 > pos_lo || k0 < first_hi || unit_bad;
+          go = __all_sync(0xffffffffu, wait(&s_full[2 * s + u], (ns >> 1) & 1u));
+          if (!go) break;
+          tc::fence_after_sync();
+          float y[64];
+          tc::tmem_ld32xN<2>(ts + u * 64, y);
+          if (masked) {
+            const int hi = pos - k0, lo = first - k0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= fo;
-              tc::tmem_st32(to + 32 * q, o);
+            for (int e = 0; e < 64; ++e) y[e] = e <= hi && e >= lo ? y[e] : -INFINITY;
+            if (unit_bad) {
+              for (int t = k0; t < k0 + 64; t += 16) {  // (blocks are multiples of 16 tokens)
+                const int i = t >> shift;
+                if (i < nblk && table[i] >= 0 && table[i] < a.pool.blocks) continue;
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  if (e >> 4 == (t - k0) >> 4) y[e] = -INFINITY;
+              }
             }
           }
-        }
-        const float2 sc2 = make_float2(scl, scl);
-        const float mu = (m == -INFINITY ? 0.f : m) - (Q8 ? (float)df + kUp : 0.f);
-        const float2 mu2 = make_float2(-mu, -mu);
-        float2 la[4];
+          float mx[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) la[q] = make_float2(0.f, 0.f);
+          for (int e = 4; e < 60; e += 8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pw[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
-            t.x = ex2_approx(t.x);
-            t.y = ex2_approx(t.y);
-            la[e & 3] = fadd2(la[e & 3], t);
-            pw[e] = Q8 ? pack_f16x2(t.x, t.y) : pack_bf16x2(t.x, t.y);
+            for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], y[e + q], y[e + 4 + q]);
           }
-          tmem_st16(ts + 16 * q, pw);
+          float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          top = fmaxf(max3(top, y[60], y[61]), fmaxf(y[62], y[63])) * scl;
+          const bool start = j == 0 && u == 0;
+          const bool need = top > m + kTau || start;
+          if (__any_sync(0xffffffffu, need || (fv != 1.f && u == 0))) {
+            const float mn = need ? fmaxf(top, m) : m;
+            const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+            m = mn;
+            l *= f;
+            const float fo = u == 0 ? f * fv : f;
+            if (!start) {  // O_s, once the half before this one is in it
+              go = __all_sync(0xffffffffu, wait(&pv_done[s], (ns - 1) & 1u));
+              if (!go) break;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                float o[32];
+                tc::tmem_ld32(to + 32 * q, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= fo;
+                tc::tmem_st32(to + 32 * q, o);
+              }
+            }
+          }
+          const float2 sc2 = make_float2(scl, scl);
+          const float mu = (m == -INFINITY ? 0.f : m) - (Q8 ? (float)df + kUp : 0.f);
+          const float2 mu2 = make_float2(-mu, -mu);
+          float2 la[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) la[q] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
+              t.x = ex2_approx(t.x);
+              t.y = ex2_approx(t.y);
+              la[e & 3] = fadd2(la[e & 3], t);
+              pw[e] = Q8 ? pack_f16x2(t.x, t.y) : pack_bf16x2(t.x, t.y);
+            }
+            tmem_st16(ts + u * 64 + 16 * q, pw);
+          }
+          tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_ready[2 * s + u]);
+          const float2 l2 = fadd2(fadd2(la[0], la[1]), fadd2(la[2], la[3]));
+          l += (l2.x + l2.y) * (Q8 ? exp2i(-df - (int)kUp) : 1.f);
         }
-        tmem_st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[s]);
-        const float2 l2 = fadd2(fadd2(la[0], la[1]), fadd2(la[2], la[3]));
-        l += (l2.x + l2.y) * (Q8 ? exp2i(-df - (int)kUp) : 1.f);
       }
       if (!go) break;
       // ---- the rows' results
@@ -440,7 +465,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to bf16 tiles
-    regs_dec<72>();
+    regs_dec<80>();
     int c = 0;
     bool go = true;
     for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
@@ -469,7 +494,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 template <int D, bool Q8>
 cudaError_t launch_rows(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream_t st) {
   cudaError_t e = set_smem_once<pool_rows_kernel<D, Q8>>(RowsSmem<D, Q8>::bytes);
-  // 128 (40 + 232 + 232) = 384 * 168 and 128 (40 + 200 + 200 + 72) = 512 * 128
+  // 128 (104 + 200 + 200) = 384 * 168 and 128 (80 + 176 + 176 + 80) = 512 * 128
   if (e == cudaSuccess) e = check_registers<pool_rows_kernel<D, Q8>>(Q8 ? 128 : 168);
   if (e == cudaSuccess) e = launch_plan<kTM, kKT>(a, st);
   if (e != cudaSuccess) return e;

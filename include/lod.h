@@ -503,7 +503,7 @@ int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, s
  * that holds one may also reach other new tokens of the same call that lie
  * within 256 query rows of one that sees it; keys that no query of a sequence
  * sees (before every window, behind the length) are never used.
- * With bits = 8 and more than 64 query rows (max_new * Hq/Hkv), a key or value
+ * With bits = 8 and more than 32 query rows (max_new * Hq/Hkv), a key or value
  * row is taken relative to the largest row of its 128 tokens and loses
  * precision when it is smaller than 2^-14 of it.
  * Keys in a bad block are left out; a row that sees no key then, and every
