@@ -19,13 +19,14 @@ struct RowsSmem {
   static constexpr size_t off_KV = off_Q + 2 * kTile;  // ring: K, V of a key tile take turns
   static constexpr size_t off_raw = off_KV + (size_t)kStages * kTile;
   static constexpr size_t off_bar = off_raw + 2 * kRaw;
-  static constexpr int kBars = 2 * kStages + 6 + 4 + 4 + 2 + 2 + 2 + 1;
+  static constexpr int kBars = 2 * kStages + 6 + 4 + 4 + 2 + 2 + 2 + 2;
   static constexpr size_t off_info = off_bar + 8 * kBars + 8;  // int [2][16] a tile's largest exponents, [2][16] its blocks
   static constexpr size_t bytes = off_info + 256 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Roles: warp 0 copies of keys, warp 2 of values, warp 1 MMA issue; warps 4-7
+// Roles: warp 0 copies, warps 1 and 2 the MMAs of query tiles 0 and 1 (one
+// issuer for both took 1000 cycles a step of 512 to 640 cycles' work); warps 4-7
 // and 8-11 the softmax of query tiles 0 and 1 (a thread per row); with an
 // 8-bit pool warps 12-15 turn codes into f16 tiles and warp 3 their exponents
 // into factors.  Such a tile's rows are taken relative to its largest exponent, C: the keys' 2^C
@@ -34,9 +35,9 @@ struct RowsSmem {
 //
 // Tensor memory: S_0, S_1 (fp32, 128 columns each; the weights P_s, bf16
 // pairs, overwrite the first half of each 64-column half of S_s), O_0, O_1.
-// Scores, weights and sums go by halves of 64 keys: for each half u the MMA
-// warp issues, for query tile s = 0, 1, O_s += P_s V_j (half u), then S_s =
-// Q_s K_{j+1}^T (half u), so a softmax warpgroup works on one half while the
+// Scores, weights and sums go by halves of 64 keys: for each half u the
+// issuer of query tile s gives O_s += P_s V_j (half u), then S_s = Q_s
+// K_{j+1}^T (half u), so a softmax warpgroup works on one half while the
 // MMAs of its other half run.  (With one buffer of 128 keys a warpgroup waited
 // 1550 of every 3650 cycles for its own MMAs.)
 // The softmax warps rescale O_s themselves, and only when a row's maximum has
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   uint64_t* pv_done = q_full + 2;
   uint64_t* o_full = pv_done + 2;
   uint64_t* fin = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* info_s = reinterpret_cast<int*>(sm + S::off_info);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], Q8 ? 4 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // one of each query tile
     }
     for (int i = 0; i < 2; ++i) {  // (keys', values')
       mbar_init(&raw_full[i], 1);
@@ -82,12 +83,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       mbar_init(&q_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
+      mbar_init(&fin[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);
     }
-    mbar_init(fin, 1);
     *abort_s = 0;
     fence_mbar_init();
     if (!Q8) {
@@ -109,121 +110,127 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 
   if (warp < 4) {
     regs_dec<Q8 ? 80 : 104>();
-    if (warp == 0 || warp == 2) {
-      // ============================================================ copies of keys, of values
-      const int kv = warp >> 1;
+    if (warp == 0) {
+      // ============================================================ copies
       int t = 0;  // key tiles; the ring takes their keys and values in turn
       bool go = true;
       for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
         Feed f(a, w.u.b, w.s.len, w.kt0, w.kt1);
-        const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-        const uint8_t* exps = kv ? a.pool.Ve : a.pool.Ke;
         const int Hkv = a.pool.Hkv, h = w.u.h;
-        for (int kt = w.kt0; kt < w.kt1; f.advance(), ++kt, ++t) {
+        for (int kt = w.kt0; kt < w.kt1 && go; f.advance(), ++kt, ++t) {
           const unsigned ok = __ballot_sync(0xffffffffu, f.cur >= 0);
           const int rows = __popc(ok) << shift;
           const int row = (f.cur * Hkv + h) << shift;  // (a pool has fewer than 2^31 rows)
-          if constexpr (Q8) {
-            if (t >= 1 && !(go = wait(&raw_empty[kv], (uint32_t)(t - 1) & 1u))) break;
-            unsigned char* dst = sm + S::off_raw + kv * S::kRaw;
-            if (lane == 0) {
-              info_s[32 + kv * 16 + (t & 15)] = (int)ok;
-              if (rows) mbar_arrive_expect(&raw_full[kv], (uint32_t)rows * (D + 1));
-              else mbar_arrive(&raw_full[kv]);
-            }
-            __syncwarp();
-            if (f.cur >= 0) {
-              bulk_g2s(dst + (lane << shift) * D, codes + (int64_t)row * D, (uint32_t)D << shift, &raw_full[kv]);
-              bulk_g2s(dst + 128 * D + (lane << shift), exps + row, 1u << shift, &raw_full[kv]);
-            }
-          } else {
-            const int c = 2 * t + kv, st = c % NS;
-            if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
-            unsigned char* d = sm + S::off_KV + (size_t)st * S::kTile + (lane << shift) * 128;
-            if (lane == 0) {
-              if (rows) mbar_arrive_expect(&full[st], (uint32_t)rows * D * 2);
-              else mbar_arrive(&full[st]);
-            }
-            __syncwarp();
-            if (f.cur >= 0) {
-              const CUtensorMap* map = kv ? &maps.V : &maps.K;
-              tma_load_box(d, map, 0, row, &full[st]);
-              if (D == 128) tma_load_box(d + kHalfBytes, map, 64, row, &full[st]);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            if constexpr (Q8) {
+              if (t >= 1 && !(go = wait(&raw_empty[kv], (uint32_t)(t - 1) & 1u))) break;
+              unsigned char* dst = sm + S::off_raw + kv * S::kRaw;
+              if (lane == 0) {
+                info_s[32 + kv * 16 + (t & 15)] = (int)ok;
+                if (rows) mbar_arrive_expect(&raw_full[kv], (uint32_t)rows * (D + 1));
+                else mbar_arrive(&raw_full[kv]);
+              }
+              __syncwarp();
+              if (f.cur >= 0) {
+                const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
+                bulk_g2s(dst + (lane << shift) * D, codes + (int64_t)row * D, (uint32_t)D << shift, &raw_full[kv]);
+                bulk_g2s(dst + 128 * D + (lane << shift), (kv ? a.pool.Ve : a.pool.Ke) + row, 1u << shift, &raw_full[kv]);
+              }
+            } else {
+              const int c = 2 * t + kv, st = c % NS;
+              if (c >= NS && !(go = wait(&empty[st], (uint32_t)(c / NS - 1) & 1u))) break;
+              unsigned char* d = sm + S::off_KV + (size_t)st * S::kTile + (lane << shift) * 128;
+              if (lane == 0) {
+                if (rows) mbar_arrive_expect(&full[st], (uint32_t)rows * D * 2);
+                else mbar_arrive(&full[st]);
+              }
+              __syncwarp();
+              if (f.cur >= 0) {
+                const CUtensorMap* map = kv ? &maps.V : &maps.K;
+                tma_load_box(d, map, 0, row, &full[st]);
+                if (D == 128) tma_load_box(d + kHalfBytes, map, 64, row, &full[st]);
+              }
             }
           }
         }
       }
       __syncwarp();
       if (*abort_s && lane == 0) {  // copies still in flight land before the CTA ends
-        for (int i = t - 1; i >= 0 && i >= t - (Q8 ? 1 : NS); --i) {
-          const int c = 2 * i + kv;
-          (void)mbar_wait(Q8 ? &raw_full[kv] : &full[c % NS], (uint32_t)(Q8 ? i : c / NS) & 1u, a.status);
-        }
+        // (t counts a tile of which only the keys may have been asked for:
+        // the wait for its values then runs out)
+        for (int i = t - 1; i >= 0 && i >= t - (Q8 ? 1 : NS); --i)
+          for (int kv = 0; kv < 2; ++kv)
+            (void)mbar_wait(Q8 ? &raw_full[kv] : &full[(2 * i + kv) % NS], (uint32_t)(Q8 ? i : (2 * i + kv) / NS) & 1u,
+                            a.status);
       }
-    } else if (warp == 1) {
-      // ============================================================ MMA issue
+    } else if (warp < 3) {
+      // ============================================================ MMA issue, query tile s
+      const int s = warp - 1;
       const uint32_t lead = elect_one();
       const uint32_t idS = Q8 ? idesc_f16(128, 64, false, false) : tc::idesc_bf16(128, 64, false, false);
       const uint32_t idO = Q8 ? idesc_f16(128, D, false, true) : tc::idesc_bf16(128, D, false, true);
-      const uint32_t qb = smem_u32(sm + S::off_Q), kvb = smem_u32(sm + S::off_KV);
-      int c = 0;                                // ring position of the next K tile (V follows it)
-      uint32_t np[2] = {0, 0}, nq[2] = {0, 0};  // weights (of key tiles) and query tiles taken
+      const uint32_t kvb = smem_u32(sm + S::off_KV);
+      const uint64_t qd = tc::desc_kmajor_sw128(smem_u32(sm + S::off_Q) + s * S::kTile);
+      const uint64_t kd0 = tc::desc_kmajor_sw128(kvb), vd0 = tc::desc_mnmajor_sw128(kvb, kHalfBytes);
+      const uint32_t ts = tmem + s * 128, to = tmem + kColO + s * 128;
+      int c = 0;                 // ring position of the next K tile (V follows it)
+      uint32_t np = 0, nq = 0;   // weights (of key tiles) and query tiles taken
       bool go = true, any = false;
       auto uniform = [&](bool x) { return (bool)__all_sync(0xffffffffu, x); };
       auto full_wait = [&](int x) { return uniform(wait(&full[x % NS], (uint32_t)(x / NS) & 1u)); };
-      auto scores = [&](int s, int u, int x) {  // S_s, half u: Q_s K^T, K at ring position x
-        const uint64_t qd = tc::desc_kmajor_sw128(qb + s * S::kTile);
-        const uint64_t kd = tc::desc_kmajor_sw128(kvb + (uint32_t)(x % NS) * S::kTile + u * 64 * 128);
+      auto scores = [&](int u, int x) {  // S_s, half u: Q_s K^T, K at ring position x
+        const uint64_t kd = kd0 + ((uint32_t)(x % NS) * (S::kTile >> 4) + u * (64 * 128 >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {  // (the address field of a descriptor counts 16 bytes)
           const uint32_t o = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-          mma_ss(lead, tmem + s * 128 + u * 64, qd + o, kd + o, idS, kk > 0);
+          mma_ss(lead, ts + u * 64, qd + o, kd + o, idS, kk > 0);
         }
         mma_commit_if(lead, &s_full[2 * s + u]);
         any = true;
       };
       for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
-        const int tiles = w.nrow > 128 ? 2 : 1;
         const int T = w.kt1 - w.kt0;
-        for (int s = 0; s < tiles && go; ++s) go = uniform(wait(&q_full[s], nq[s]++ & 1u));
-        if (!go || !(go = full_wait(c))) break;
+        if (s * 128 >= w.nrow) {  // no second query tile: its share of the ring is given back as it fills
+          for (int j = 0; j < 2 * T && go; ++j, ++c) {
+            go = full_wait(c);
+            if (go && lane == 0) mbar_arrive(&empty[c % NS]);
+          }
+          continue;
+        }
+        if (!(go = uniform(wait(&q_full[s], nq++ & 1u)) && full_wait(c))) break;
         tc::fence_after_sync();
-        for (int u = 0; u < 2; ++u)
-          for (int s = 0; s < tiles; ++s) scores(s, u, c);
+        scores(0, c);
+        scores(1, c);
         mma_commit_if(lead, &empty[c % NS]);
-        for (int j = 0; j < T && go; ++j, c += 2) {
+        for (int j = 0; j < T && go; ++j, ++np, c += 2) {
+          const uint64_t vd = vd0 + (uint32_t)((c + 1) % NS) * (S::kTile >> 4);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            for (int s = 0; s < tiles && go; ++s) {
-              go = uniform(wait(&p_ready[2 * s + u], np[s] & 1u)) && (u + s > 0 || full_wait(c + 1));
-              if (!go) break;
-              np[s] += u;
-              tc::fence_after_sync();
-              const uint64_t vd = tc::desc_mnmajor_sw128(kvb + (uint32_t)((c + 1) % NS) * S::kTile, kHalfBytes);
+            go = uniform(wait(&p_ready[2 * s + u], np & 1u)) && (u == 1 || full_wait(c + 1));
+            if (!go) break;
+            tc::fence_after_sync();
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(lead, tmem + kColO + s * 128, tmem + s * 128 + u * 64 + 8 * kk, vd + (4 * u + kk) * (2048 >> 4),
-                       idO, j > 0 || u + kk > 0);
-              mma_commit_if(lead, &pv_done[s]);
-              const bool last = u == 1 && s == tiles - 1;
-              if (last) mma_commit_if(lead, &empty[(c + 1) % NS]);
-              if (j + 1 < T) {
-                if (u + s == 0) {
-                  if (!(go = full_wait(c + 2))) break;
-                  tc::fence_after_sync();
-                }
-                scores(s, u, c + 2);
-                if (last) mma_commit_if(lead, &empty[(c + 2) % NS]);
-              } else if (u == 1) {
-                mma_commit_if(lead, &o_full[s]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(lead, to, ts + u * 64 + 8 * kk, vd + (4 * u + kk) * (2048 >> 4), idO, j > 0 || u + kk > 0);
+            mma_commit_if(lead, &pv_done[s]);
+            if (u == 1) mma_commit_if(lead, &empty[(c + 1) % NS]);
+            if (j + 1 < T) {
+              if (u == 0) {
+                if (!(go = full_wait(c + 2))) break;
+                tc::fence_after_sync();
               }
+              scores(u, c + 2);
+              if (u == 1) mma_commit_if(lead, &empty[(c + 2) % NS]);
+            } else if (u == 1) {
+              mma_commit_if(lead, &o_full[s]);
             }
           }
         }
       }
       if (any) {
-        mma_commit_if(lead, fin);
-        (void)mbar_wait(fin, 0, a.status);
+        mma_commit_if(lead, &fin[s]);
+        (void)mbar_wait(&fin[s], 0, a.status);
       }
       __syncwarp();
     } else if (Q8) {
