@@ -384,12 +384,13 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], y[e + q], y[e + 4 + q]);
           }
-          float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-          top = fmaxf(max3(top, y[60], y[61]), fmaxf(y[62], y[63])) * scl;
+          float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], y[60]);
+          top = max3(max3(top, y[61], y[62]), y[63], y[63]) * scl;
+          if (top != top) l = NAN;  // a NaN score: the row's results are NaN, whatever its weights become
           const bool start = j == 0 && u == 0;
           const bool need = top > m + kTau || start;
           if (__any_sync(0xffffffffu, need || (fv != 1.f && u == 0))) {
-            const float mn = need ? fmaxf(top, m) : m;
+            const float mn = need ? fmaxf(top, m) : m;  // (drops a NaN)
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
             m = mn;
             l *= f;
@@ -420,8 +421,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
-              t.x = ex2_approx(t.x);
-              t.y = ex2_approx(t.y);
+              // the exponentials are shared out: the special-function unit
+              // takes 8 cycles for a warp's 32, the FMA pipe 7
+              if (e % 8 == 1 || e % 8 == 3 || e % 8 == 6) {
+                t = exp2_fma2(t);
+              } else {
+                t.x = ex2_approx(t.x);
+                t.y = ex2_approx(t.y);
+              }
               la[e & 3] = fadd2(la[e & 3], t);
               pw[e] = Q8 ? pack_f16x2(t.x, t.y) : pack_bf16x2(t.x, t.y);
             }
