@@ -93,12 +93,22 @@ struct PoolAttendArgs {
   int64_t* Wb;             // [B + 1] key tiles before each sequence (all heads)
   int32_t* RT;             // [B + 1] row tiles before each sequence (one head)
   int32_t* pre;            // [RT[B]] key tiles of the sequence (one head) before each row tile
-  float* part;             // [ctas][2][TM][d] partial sums
-  float2* ml;              // [ctas][2][TM] their (max, sum), log2 units
+  float* part;             // [parts][2][TM][d] partial sums
+  float2* ml;              // [parts][2][TM] their (max, sum), log2 units
   int ctas;
   int min_share;           // key tiles a CTA takes at least
   int planned;             // 1: Wb, RT, pre were written by the plan kernel
+  // The kernel of many rows takes the list in rounds: a CTA's parts are c, c +
+  // ctas, ... of ctas * rounds.  The CTAs of a round then read about
+  // kRoundBytes of the cache between them, which stays in L2 while the
+  // row tiles of a head sweep over it at offsets of their own (a 2048-token
+  // chunk over 128K read 15.8 GB from DRAM in one round, for 0.54 GB of cache).
+  int max_rounds;
+  int32_t* rounds;         // (null: one round)
+  int row_bytes;           // stored bytes of a key and its value
 };
+constexpr int64_t kRoundBytes = (int64_t)64 << 20;
+constexpr int kMaxRounds = 8;
 
 // Sequence b of a batch, checked: r0 = first packed row, n = new tokens (0
 // when the sequence is refused), len = tokens.
@@ -170,7 +180,15 @@ __device__ __forceinline__ Unit find_unit(const PoolAttendArgs& a, const int64_t
   return u;
 }
 
-// A CTA's walk through its part [w, w1) of the list, one piece of a unit at a
+// Parts of the list, and the entries of one.
+__device__ __forceinline__ int list_parts(const PoolAttendArgs& a) { return a.ctas * (a.rounds ? *a.rounds : 1); }
+__device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t total) {
+  const int parts = list_parts(a);
+  const int64_t s = (total + parts - 1) / parts;
+  return s > a.min_share ? s : a.min_share;
+}
+
+// A CTA's walk through a part [w, w1) of the list, one piece of a unit at a
 // time: key tiles [kt0, kt1) of unit u.  Every role of a CTA takes the same walk.
 template <int TM, int KT>
 struct Walk {
@@ -181,11 +199,9 @@ struct Walk {
   int64_t pe;       // end of the piece
   int nt, kt0, kt1, nrow;
 
-  __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* Wb, int cta) : a(args) {
-    const int64_t total = Wb[a.batch.B];
-    int64_t share = (total + a.ctas - 1) / a.ctas;
-    if (share < a.min_share) share = a.min_share;
-    w0 = w = cta * share;
+  __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* Wb, int part) : a(args) {
+    const int64_t total = Wb[a.batch.B], share = list_share(a, total);
+    w0 = w = part * share;
     w1 = w0 + share < total ? w0 + share : total;
     if (w < w1) {
       u = find_unit<TM, KT>(a, Wb, w);
@@ -226,7 +242,7 @@ struct Walk {
     } while (kt0 == kt1);
   }
   __device__ __forceinline__ bool whole() const { return w <= u.first() && pe == uend; }
-  __device__ __forceinline__ int slot(int cta) const { return 2 * cta + (u.first() >= w0 ? 1 : 0); }
+  __device__ __forceinline__ int slot(int part) const { return 2 * part + (u.first() >= w0 ? 1 : 0); }
 };
 
 // Sequences a CTA can lay out by itself (one row tile each): the list's
@@ -263,11 +279,6 @@ __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb
   __syncthreads();
 }
 
-__device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t total) {
-  const int64_t s = (total + a.ctas - 1) / a.ctas;
-  return s > a.min_share ? s : a.min_share;
-}
-
 // Rows of refused sequences: out = 0, lse = -inf.  Every CTA of the grid calls
 // this with all its threads; the CTAs share the sequences out.
 template <typename T, int D>
@@ -297,9 +308,15 @@ struct PoolShape {
   int kind;  // 0: CUDA cores (fp32); 1: tensor cores, 256 rows a unit; 2: tensor cores, few rows
   int TM, KT, ctas;
   bool inline_plan;
+  int max_rounds;
   size_t off_plan, off_ml, off_part, total;  // workspace offsets
 };
-PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms);
+// Stored bytes of a key and its value.
+inline int pool_row_bytes(int dtype, int bits, int d) {
+  return 2 * (bits == 8 ? d + 1 : d * (dtype == LOD_DTYPE_F32 ? 4 : 2));
+}
+PoolShape pool_shape(int dtype, int bits, int d, int Hkv, int G, int B, int64_t capacity, int64_t N, int64_t max_new,
+                     int sms);
 // TMA tensor maps of a bf16 pool's K and V: rows x d, boxes of 64 channels x one block.
 struct __align__(64) PoolMaps {
   CUtensorMap K, V;

@@ -132,7 +132,8 @@ int32_t check_status(const uint32_t* status) {
 }
 
 lod::PoolShape shape_of(const lod_pool* p, const lod_batch* b) {
-  return lod::pool_shape(p->dtype, p->bits, p->d, p->Hq / p->Hkv, b->B, b->N, b->max_new, num_sms());
+  return lod::pool_shape(p->dtype, p->bits, p->d, p->Hkv, p->Hq / p->Hkv, b->B, (int64_t)b->max_blocks * p->block, b->N,
+                         b->max_new, num_sms());
 }
 
 }  // namespace
@@ -298,10 +299,13 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
     a.Wb = reinterpret_cast<int64_t*>(w + s.off_plan);
     a.RT = reinterpret_cast<int32_t*>(a.Wb + batch->B + 1);
     a.pre = a.RT + batch->B + 1;
+    if (s.kind == 1) a.rounds = reinterpret_cast<int32_t*>(w + s.off_ml) - 4;  // the plan's last 16 bytes
   }
   a.ml = reinterpret_cast<float2*>(w + s.off_ml);
   a.part = reinterpret_cast<float*>(w + s.off_part);
   a.ctas = s.ctas;
+  a.max_rounds = s.max_rounds;
+  a.row_bytes = lod::pool_row_bytes(pool->dtype, pool->bits, pool->d);
   a.min_share = 1;
   lod::PoolMaps maps;
   const bool tma = s.kind != 0 && pool->bits == 0;

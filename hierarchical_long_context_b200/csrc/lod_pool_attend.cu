@@ -240,8 +240,10 @@ cudaError_t launch_simt_d(const PoolAttendArgs& a, int TM, int bits, cudaStream_
 
 }  // namespace
 
-PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_t max_new, int sms) {
+PoolShape pool_shape(int dtype, int bits, int d, int Hkv, int G, int B, int64_t capacity, int64_t N, int64_t max_new,
+                     int sms) {
   PoolShape s = {};
+  s.max_rounds = 1;
   const int64_t rows = max_new * G;
   s.kind = dtype != LOD_DTYPE_BF16 ? 0 : rows > (bits == 8 ? 32 : 64) ? 1 : 2;
   if (s.kind == 2) {
@@ -254,6 +256,8 @@ PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_
     s.KT = 128;
     s.ctas = sms;
     s.inline_plan = false;
+    const int64_t bytes = capacity * B * Hkv * pool_row_bytes(dtype, bits, d);
+    s.max_rounds = (int)(bytes > kRoundBytes * kMaxRounds ? kMaxRounds : (bytes + kRoundBytes - 1) / kRoundBytes);
   } else {
     s.TM = max_new * G <= 16 ? 16 : 64;
     s.KT = 64;
@@ -263,10 +267,10 @@ PoolShape pool_shape(int dtype, int bits, int d, int G, int B, int64_t N, int64_
   const int64_t tiles = N * G / s.TM + B;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   s.off_plan = kWsHeader;
-  size_t plan = s.inline_plan ? 0 : (size_t)(B + 1) * 16 + (size_t)tiles * 4;
+  size_t plan = s.inline_plan ? 0 : (size_t)(B + 1) * 16 + (size_t)tiles * 4 + 16;
   s.off_ml = s.off_plan + up(plan);
-  s.off_part = s.off_ml + up((size_t)s.ctas * 2 * s.TM * sizeof(float2));
-  s.total = s.off_part + up((size_t)s.ctas * 2 * s.TM * d * sizeof(float));
+  s.off_part = s.off_ml + up((size_t)s.ctas * s.max_rounds * 2 * s.TM * sizeof(float2));
+  s.total = s.off_part + up((size_t)s.ctas * s.max_rounds * 2 * s.TM * d * sizeof(float));
   return s;
 }
 

@@ -86,12 +86,33 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
     at += total;
   }
   if (threadIdx.x == 0) a.Wb[0] = 0;
+  if (a.rounds) {
+    int64_t keys = 0;
+    for (int b0 = 0; b0 < B; b0 += 1024) {
+      const int b = b0 + threadIdx.x;
+      int64_t n = 0;
+      if (b < B) {
+        const SeqView s = seq_view(a.batch, a.pool.shift, b);
+        if (s.n > 0) n = a.window > 0 && s.len > a.window + s.n ? a.window + s.n : s.len;
+      }
+      block_scan(n, ws, &total);
+      keys += total;
+    }
+    if (threadIdx.x == 0) {
+      const int64_t r = (keys * a.pool.Hkv * a.row_bytes + kRoundBytes - 1) / kRoundBytes;
+      // (never rounds of fewer than 64 tiles a CTA)
+      const int64_t most = a.Wb[B] / ((int64_t)a.ctas * 64);
+      int64_t n = r < most ? r : most;
+      if (n > a.max_rounds) n = a.max_rounds;
+      *a.rounds = n < 1 ? 1 : (int32_t)n;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- merge
 
-// Joins the pieces of the unit whose first tile lies in CTA c's part of the
-// list and whose last lies behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
+// Joins the pieces of the unit whose first tile lies in part c of the list and
+// whose last lies behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
 // in that order, so the result does not depend on which CTA ran when.  One
 // warp per row, blockIdx.y picks 16 rows.
 template <typename T, int D, int TM, int KT>
@@ -102,6 +123,7 @@ __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
     plan_inline<TM, KT>(a, wb_s);
     Wb = wb_s;
   }
+  if ((int)blockIdx.x >= list_parts(a)) return;
   const int64_t total = Wb[a.batch.B], share = list_share(a, total);
   const int64_t w0 = blockIdx.x * share, w1 = w0 + share;
   if (w1 >= total) return;
@@ -156,7 +178,7 @@ cudaError_t launch_plan(const PoolAttendArgs& a, cudaStream_t st) {
 
 template <typename T, int D, int TM, int KT>
 cudaError_t launch_merge(const PoolAttendArgs& a, cudaStream_t st) {
-  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas, (TM + 15) / 16), 256, 0, st>>>(a);
+  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas * a.max_rounds, (TM + 15) / 16), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 

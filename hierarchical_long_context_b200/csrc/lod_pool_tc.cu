@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   constexpr uint32_t kColO = 256;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_or_abort(bar, parity, abort_s, a.status); };
-  const int shift = a.pool.shift;
+  const int shift = a.pool.shift, parts = list_parts(a);
   const int per_tile = kKT >> shift;  // blocks of a key tile
 
   if (warp < 4) {
@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       // ============================================================ copies
       int t = 0;  // key tiles; the ring takes their keys and values in turn
       bool go = true;
-      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+      for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
         Feed f(a, w.u.b, w.s.len, w.kt0, w.kt1);
         const int Hkv = a.pool.Hkv, h = w.u.h;
         for (int kt = w.kt0; kt < w.kt1 && go; f.advance(), ++kt, ++t) {
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         mma_commit_if(lead, &s_full[2 * s + u]);
         any = true;
       };
-      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+      for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
         const int T = w.kt1 - w.kt0;
         if (s * 128 >= w.nrow) {  // no second query tile: its share of the ring is given back as it fills
           for (int j = 0; j < 2 * T && go; ++j, ++c) {
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       // ============================================================ row factors
       int t = 0;
       bool go = true;
-      for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+      for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
         for (int kt = w.kt0; kt < w.kt1 && go; ++kt, ++t) {
           for (int kv = 0; kv < 2; ++kv) {
             if (!(go = __all_sync(0xffffffffu, wait(&raw_full[kv], (uint32_t)t & 1u)))) break;
@@ -273,7 +276,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     uint32_t ns = 0, no = 0;  // key halves and outputs taken
     int c = 0;                // ring position of the next key tile's K
     bool go = true;
-    for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+    for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
       const int T = w.kt1 - w.kt0;
       if (s * 128 >= w.nrow) {
         c += 2 * T;
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const bool whole = w.whole();
       const float unit = Q8 ? exp2i(cv - 127 - (int)kUp) : 1.f;
       const float inv = l > 0.f || l != l ? unit / l : 0.f;
-      const int64_t at = (int64_t)w.slot(blockIdx.x) * kTM + s * 128 + r;
+      const int64_t at = (int64_t)w.slot(part) * kTM + s * 128 + r;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -482,7 +486,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     regs_dec<80>();
     int c = 0;
     bool go = true;
-    for (Walk<kTM, kKT> w(a, a.Wb, blockIdx.x); w.more() && go; w.next()) {
+    for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
       for (int x = 0; x < 2 * (w.kt1 - w.kt0); ++x, ++c) {
         go = __all_sync(0xffffffffu, wait(&fac_full[c & 1], (uint32_t)(c >> 1) & 1u) &&
                                          (c < NS || wait(&empty[c % NS], (uint32_t)(c / NS - 1) & 1u)));

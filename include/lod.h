@@ -481,9 +481,10 @@ int32_t lod_pool_read(const lod_pool* pool, const lod_batch* batch, int64_t t_be
                       void* V, const int64_t kv_strides[3], uint32_t* status, lod_stream_t stream);
 
 /*
- * Workspace bytes of lod_pool_attend for a batch of at most batch->B
- * sequences, N rows and max_new new tokens of one sequence (device pointers
- * of pool and batch are not looked at).  256-byte aligned device memory,
+ * Workspace bytes of lod_pool_attend for a batch of exactly these B,
+ * max_blocks, N and max_new (device pointers of pool and batch are not looked
+ * at; a larger workspace serves as well, and one of the largest of several
+ * calls serves them all).  256-byte aligned device memory,
  * zeroed once after allocation; its first word is the status word of
  * lod_get_status.
  */
