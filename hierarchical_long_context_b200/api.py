@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -44,6 +45,14 @@ class Params:
             _DT[self.dtype], self.B, self.Hq, self.Hkv, self.d, self.chunk, self.page,
             self.clusters, self.kmeans_iters, self.top_groups, self.top_pages, self.window,
             self.sinks, self.kv_bits, self.seed & (2**64 - 1), self.scale, self.head_shard, self.Tmax)
+
+    def ref(self):
+        """A reference to the C struct, kept (the fields are frozen)."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = ctypes.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
 
     @property
     def page_slots(self) -> int:
@@ -214,7 +223,13 @@ def lod_prefill(params: Params, q, q_begin: int, K, V, index: Index, out=None, l
 
 # ---------------------------------------------------------------- projections into a cache, block pool
 
-_I2, _I3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+# The calls below are made once a layer and token, for a few microseconds of GPU
+# work each: their structs, stride arrays and references are built once.
+
+@lru_cache(maxsize=1024)
+def _strides(st: tuple):
+    """Element strides as the C array (read only)."""
+    return (ctypes.c_int64 * len(st))(*st)
 
 
 class Rope:
@@ -232,12 +247,15 @@ class Rope:
         self._c = _lib.lod_rope(_addr(q_norm), _addr(k_norm), _addr(inv_freq), eps,
                                 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), 0)
         self._ref = ctypes.byref(self._c)
+        self._fits = None  # the (d, dtype) the weights were last checked against
 
     def ref(self, d: int, dtype: torch.dtype):
         """The C struct, after checking the weights against the rows they are for."""
-        for w in (self.q_norm, self.k_norm):
-            if w is not None and (w.shape[0] != d or w.dtype != dtype):
-                raise ValueError("norm weights must be [%d] %s" % (d, dtype))
+        if self._fits != (d, dtype):
+            for w in (self.q_norm, self.k_norm):
+                if w is not None and (w.shape[0] != d or w.dtype != dtype):
+                    raise ValueError("norm weights must be [%d] %s" % (d, dtype))
+            self._fits = (d, dtype)
         return self._ref
 
 
@@ -261,6 +279,7 @@ class Pool:
                     raise ValueError("Ke and Ve must be contiguous uint8 [blocks, Hkv, block]")
         self.K, self.V, self.Ke, self.Ve, self.dtype, self.Hq = K, V, Ke, Ve, dtype, Hq
         blocks, self.Hkv, self.block, self.d = K.shape
+        self.device = K.device
         self._c = _lib.lod_pool(_DT[dtype], 0 if Ke is None else 8, Hq, self.Hkv, self.d, self.block, blocks,
                                 _addr(K), _addr(V), _addr(Ke), _addr(Ve))
         self._ref = ctypes.byref(self._c)
@@ -295,7 +314,7 @@ class PoolBatch:
                                       or not new_begin.is_contiguous()):
             raise ValueError("new_begin must be a contiguous int64 [B + 1] tensor")
         self.block_table, self.seq_lens, self.new_begin = block_table, seq_lens, new_begin
-        self.tokens, self.max_new = tokens, max_new
+        self.tokens, self.max_new, self.B, self.max_blocks = tokens, max_new, B, block_table.shape[1]
         self._c = _lib.lod_batch(B, block_table.shape[1], tokens, max_new, _addr(block_table), _addr(seq_lens),
                                  _addr(new_begin))
         self._ref = ctypes.byref(self._c)
@@ -306,17 +325,21 @@ def _addr(t):
 
 
 def _rows(t, shape, dtype, name):
-    """Strides of rows with contiguous channels (all dimensions but the last)."""
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    """Strides of rows with contiguous channels (all dimensions but the last), as the C array."""
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError("%s must be %s %s; got %s %s" % (name, shape, dtype, tuple(t.shape), t.dtype))
     st = t.stride()
     if st[-1] != 1:
         raise ValueError("%s must have contiguous channels" % name)
-    return st[:-1]
+    return _strides(st[:-1])
 
 
-def _stream_handle(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream_handle(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if device.type != "cuda":
+        raise RuntimeError("the cache must be on a CUDA device, not %s" % device)
+    return torch._C._cuda_getCurrentRawStream(device.index)  # (torch.cuda.current_stream builds an object: 3 us)
 
 
 def _status_word(status):
@@ -330,27 +353,29 @@ def lod_append_rope(params: Params, rope: Rope, q, k, v, K, V, seq_lens, q_out=N
     [seq_lens - n, seq_lens) of K, V, the keys normed and rotated by `rope`, and the normed and rotated q
     [B, Hq, n, d] to q_out (which may be q).  q, k, v may be strided views of one fused projection; q None
     appends the keys and values alone.  Returns q_out."""
-    st = _kv_strides(params, K, V)
+    B, Hkv, d, dt = params.B, params.Hkv, params.d, params.dtype
+    st = K.stride()
+    if K.dtype is not dt or V.dtype is not dt or K.shape != V.shape or V.stride() != st or len(st) != 4 \
+            or st[3] != 1 or K.shape[0] != B or K.shape[1] != Hkv or K.shape[3] != d or K.shape[2] < params.Tmax:
+        _kv_strides(params, K, V)  # names what is wrong
     n = k.shape[2] if k.dim() == 4 else -1
-    ks = _rows(k, (params.B, params.Hkv, n, params.d), params.dtype, "k")
-    if _rows(v, tuple(k.shape), params.dtype, "v") != ks:
+    ks = _rows(k, (B, Hkv, n, d), dt, "k")
+    if _rows(v, (B, Hkv, n, d), dt, "v") is not ks and v.stride() != k.stride():
         raise ValueError("k and v must share strides")
-    if seq_lens.shape != (params.B,) or seq_lens.dtype != torch.int64:
+    if seq_lens.shape != (B,) or seq_lens.dtype is not torch.int64:
         raise ValueError("seq_lens must be int64 [B]")
     qs = os = None
     if q is not None:
-        shape = (params.B, params.Hq, n, params.d)
-        qs = _rows(q, shape, params.dtype, "q")
+        shape = (B, params.Hq, n, d)
+        qs = _rows(q, shape, dt, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=q.dtype, device=K.device)
-        os = _I3(*_rows(q_out, shape, params.dtype, "q_out"))
-        qs = _I3(*qs)
+            q_out = torch.empty(shape, dtype=dt, device=K.device)
+        os = _rows(q_out, shape, dt, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     check("lod_append_rope", load().lod_append_rope(
-        ctypes.byref(params.c()), rope.ref(params.d, params.dtype), _addr(q), qs, k.data_ptr(), v.data_ptr(),
-        _I3(*ks), n, K.data_ptr(), V.data_ptr(), st, seq_lens.data_ptr(), _addr(q_out), os,
-        _stream_handle(stream)))
+        params.ref(), rope.ref(d, dt), _addr(q), qs, k.data_ptr(), v.data_ptr(), ks, n, K.data_ptr(), V.data_ptr(),
+        _strides(st[:3]), seq_lens.data_ptr(), _addr(q_out), os, _stream_handle(stream, K.device)))
     return q_out
 
 
@@ -362,19 +387,19 @@ def lod_pool_append(pool: Pool, batch: PoolBatch, k, v, rope: Rope | None = None
         raise ValueError("the batch has no new_begin")
     N, d, dt = batch.tokens, pool.d, pool.dtype
     ks = _rows(k, (N, pool.Hkv, d), dt, "k")
-    if _rows(v, (N, pool.Hkv, d), dt, "v") != ks:
+    if _rows(v, (N, pool.Hkv, d), dt, "v") is not ks and v.stride() != k.stride():
         raise ValueError("k and v must share strides")
     qs = os = None
     if q is not None:
-        qs = _I2(*_rows(q, (N, pool.Hq, d), dt, "q"))
+        qs = _rows(q, (N, pool.Hq, d), dt, "q")
         if q_out is None:
             q_out = torch.empty(N, pool.Hq, d, dtype=dt, device=pool.K.device)
-        os = _I2(*_rows(q_out, (N, pool.Hq, d), dt, "q_out"))
+        os = _rows(q_out, (N, pool.Hq, d), dt, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     check("lod_pool_append", load().lod_pool_append(
         pool._ref, batch._ref, None if rope is None else rope.ref(d, dt), _addr(q), qs, k.data_ptr(), v.data_ptr(),
-        _I2(*ks), _addr(q_out), os, _status_word(status), _stream_handle(stream)))
+        ks, _addr(q_out), os, _status_word(status), _stream_handle(stream, pool.device)))
     return q_out
 
 
@@ -382,20 +407,20 @@ def lod_pool_read(pool: Pool, batch: PoolBatch, K, V, t_begin: int = 0, t_end: i
                   stream=None) -> None:
     """Read tokens [t_begin, min(t_end, seq_lens)) of every sequence into the dense cache K, V [B, Hkv, T, d] of
     the pool's dtype (t_end None: up to T)."""
-    B = batch.block_table.shape[0]
-    if K.dim() != 4 or K.shape[:2] != (B, pool.Hkv) or K.shape[3] != pool.d or K.shape != V.shape:
+    shape, st = K.shape, K.stride()
+    if len(st) != 4 or shape[0] != batch.B or shape[1] != pool.Hkv or shape[3] != pool.d or shape != V.shape:
         raise ValueError("K, V must be [B, Hkv, T, d]; got %s / %s" % (tuple(K.shape), tuple(V.shape)))
-    if K.dtype != pool.dtype or V.dtype != pool.dtype:
+    if K.dtype is not pool.dtype or V.dtype is not pool.dtype:
         raise TypeError("K/V dtype %s/%s != pool dtype %s" % (K.dtype, V.dtype, pool.dtype))
-    if K.stride() != V.stride() or K.stride(3) != 1:
+    if st != V.stride() or st[3] != 1:
         raise ValueError("K and V must share strides with a contiguous last dimension")
     if t_end is None:
-        t_end = min(K.shape[2], batch.block_table.shape[1] * pool.block)
-    if t_end > K.shape[2]:
-        raise ValueError("t_end %d behind the dense cache's %d tokens" % (t_end, K.shape[2]))
+        t_end = min(shape[2], batch.max_blocks * pool.block)
+    if t_end > shape[2]:
+        raise ValueError("t_end %d behind the dense cache's %d tokens" % (t_end, shape[2]))
     check("lod_pool_read", load().lod_pool_read(
-        pool._ref, batch._ref, t_begin, t_end, K.data_ptr(), V.data_ptr(), _I3(*K.stride()[:3]),
-        _status_word(status), _stream_handle(stream)))
+        pool._ref, batch._ref, t_begin, t_end, K.data_ptr(), V.data_ptr(), _strides(st[:3]),
+        _status_word(status), _stream_handle(stream, pool.device)))
 
 
 def pool_workspace_bytes(pool: Pool, batch: PoolBatch) -> int:
@@ -416,17 +441,17 @@ def lod_pool_attend(pool: Pool, batch: PoolBatch, q, out=None, lse=None, window:
     if batch.new_begin is None:
         raise ValueError("the batch has no new_begin")
     shape = (batch.tokens, pool.Hq, pool.d)
-    qs = _I2(*_rows(q, shape, pool.dtype, "q"))
+    qs = _rows(q, shape, pool.dtype, "q")
     if out is None:
-        out = torch.empty(shape, dtype=pool.dtype, device=pool.K.device)
-    os = _I2(*_rows(out, shape, pool.dtype, "out"))
-    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        out = torch.empty(shape, dtype=pool.dtype, device=pool.device)
+    os = _rows(out, shape, pool.dtype, "out")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [N, Hq] tensor")
     if ws is None:
         ws = pool_workspace(pool, batch)
     check("lod_pool_attend", load().lod_pool_attend(
         pool._ref, batch._ref, q.data_ptr(), qs, out.data_ptr(), os, _addr(lse), window, scale, ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream_handle(stream)))
+        ws.numel() * ws.element_size(), _stream_handle(stream, pool.device)))
     return out
 
 

@@ -84,14 +84,18 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 
 // One warp per (token, share of its heads); a row of d channels is held by
 // LPR lanes, 16 bytes each, so a pass of the warp covers 32 / LPR rows (heads)
-// of the token.  The token's angles are computed once by the warp and stay in
-// registers over its rows.  Traffic: every row is read once and written once
-// (memory bound; the arithmetic of a pass, about 100 instructions for 2 rows
-// of 128 bf16, stays below the time its 1 KB takes).
+// of the token, and kBatch passes' loads are in flight together.  The rows go
+// by kind (queries, keys, values).  For a kind, a channel's cosine is
+// multiplied by its norm weight and its sine by its partner's once, so that a
+// row takes out = rstd * (x * cw + partner * sw): the partners cross lanes as
+// the stored 16-byte words, not as floats.  Every row is read once and written
+// once (memory bound: 32768 tokens of 32 + 16 heads, 128 bf16 channels, take
+// the 805 MB in and out at the time the launch comment gives).
 template <typename T, int D, int SINK>
-__global__ void __launch_bounds__(128) append_rows_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int E = 16 / (int)sizeof(T);
   constexpr int LPR = D / E, RPW = 32 / LPR;
+  constexpr int kBatch = 4;
   __shared__ float2 tab[4][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR, e0 = li * E;
@@ -129,131 +133,152 @@ __global__ void __launch_bounds__(128) append_rows_kernel(AppendArgs a) {
       store = false;
     }
   }
+  const int64_t in_block = pos & (((int64_t)1 << a.pool.shift) - 1);
 
-  // this lane's angles and weights
-  float c[E], s[E], wq[E], wk[E];
+  // the passes of queries, keys and values, and this warp's share of them
+  const int pq = (a.Hq + RPW - 1) / RPW, pk = (a.Hkv + RPW - 1) / RPW, passes = pq + 2 * pk;
+  const int p0 = (int)((int64_t)passes * part / a.split), p1 = (int)((int64_t)passes * (part + 1) / a.split);
+
   const int half = a.use_rope ? a.rope.rot >> 1 : 0, rot = 2 * half;
   const bool inter = a.rope.interleaved != 0;
-  for (int i = lane; i < half; i += 32) tab[warp][i] = turn(pos, a.rope.freq[i]);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int e = e0 + i;
-    c[i] = 1.f;
-    s[i] = 0.f;
-    wq[i] = wk[i] = 1.f;
-    if (e < rot) {
-      const bool second = inter ? (e & 1) : e >= half;
-      const float2 cs = tab[warp][inter ? e >> 1 : second ? e - half : e];
-      c[i] = cs.x;
-      s[i] = second ? cs.y : -cs.y;
-    }
+  if (p0 < pq + pk) {
+    for (int i = lane; i < half; i += 32) tab[warp][i] = turn(pos, a.rope.freq[i]);
+    __syncwarp();
   }
-  const bool nq = a.use_rope && a.rope.wq, nk = a.use_rope && a.rope.wk;
-  if (nq) Pack<T, E>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.rope.wq) + e0), wq);
-  if (nk) Pack<T, E>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.rope.wk) + e0), wk);
   const bool by_shuffle = !inter && half % E == 0;  // the partner channels sit in one other lane
-  const int other = sub * LPR + (e0 < half ? li + half / E : li - half / E);
-  const int src = e0 < rot ? other & 31 : lane;
+  const int src = e0 >= rot ? lane : sub * LPR + (e0 < half ? li + half / E : li - half / E);
 
-  const int rows = a.Hq + 2 * a.Hkv;
-  const int passes = (rows + RPW - 1) / RPW;
-  const int p0 = (int)((int64_t)passes * part / a.split), p1 = (int)((int64_t)passes * (part + 1) / a.split);
-  auto row_ptr = [&](int r) -> const T* {
-    if (r < a.Hq) return static_cast<const T*>(a.q) + b * a.qb + t * a.qt + (int64_t)r * a.qh;
-    const bool is_k = r < a.Hq + a.Hkv;
-    const T* base = static_cast<const T*>(is_k ? a.k : a.v);
-    return base + b * a.kb + t * a.kt + (int64_t)(r - a.Hq - (is_k ? 0 : a.Hkv)) * a.kh;
-  };
-  auto fetch = [&](int p) -> uint4 {
-    const int r = p * RPW + sub;
-    return p < p1 && r < rows ? *reinterpret_cast<const uint4*>(row_ptr(r) + e0) : make_uint4(0, 0, 0, 0);
-  };
-  uint4 raw = fetch(p0);
-  for (int p = p0; p < p1; ++p) {
-    const uint4 cur = raw;
-    raw = fetch(p + 1);
-    const int r = p * RPW + sub;
-    const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hkv, live = r < rows;
-    float x[E];
-    Pack<T, E>::unpack(cur, x);
-    if (a.use_rope && __any_sync(0xffffffffu, live && !is_v)) {
-      const bool normed = is_q ? nq : nk && !is_v;
-      float rstd = 1.f;
-      if (nq || nk) {
-        float ss = 0.f;
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {  // queries, keys, values
+    const int rows = kind == 0 ? a.Hq : a.Hkv, first = kind == 0 ? 0 : kind == 1 ? pq : pq + pk;
+    const int count = kind == 0 ? pq : pk;
+    const int lo = p0 > first ? p0 - first : 0, hi = p1 < first + count ? p1 - first : count;
+    if (lo >= hi) continue;
+    const T* in = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v);
+    in += kind == 0 ? b * a.qb + t * a.qt : b * a.kb + t * a.kt;
+    const int64_t row_stride = kind == 0 ? a.qh : a.kh;
+    const T* w = !a.use_rope || kind == 2 ? nullptr : static_cast<const T*>(kind == 0 ? a.rope.wq : a.rope.wk);
+    const bool turned = a.use_rope && kind < 2;
+
+    float cw[E], sw[E];  // cosine times own weight, sine (signed) times the partner's
+    if (turned) {
+      float own[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+      for (int i = 0; i < E; ++i) own[i] = 1.f;
+      if (w) Pack<T, E>::unpack(*reinterpret_cast<const uint4*>(w + e0), own);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rstd = rsqrtf(ss * (1.f / D) + a.rope.eps);
-      }
-      float y[E], z[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) y[i] = normed ? x[i] * rstd * (is_q ? wq[i] : wk[i]) : x[i];
-      if (inter) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) z[i] = y[i ^ 1];
-      } else if (by_shuffle) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) z[i] = __shfl_sync(0xffffffffu, y[i], src);
-      } else {
-        // a pair's channels at an odd distance: the partners come from the row itself
-        const T* xr = row_ptr(live ? r : rows - 1);
-        const T* w = static_cast<const T*>(is_q ? a.rope.wq : a.rope.wk);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int e = e0 + i, pe = e < half ? e + half : e - half;
-          z[i] = 0.f;
-          if (e < rot) z[i] = Elem<T>::to_f(xr[pe]) * (normed ? rstd * Elem<T>::to_f(w[pe]) : 1.f);
+      for (int i = 0; i < E; ++i) {
+        const int e = e0 + i;
+        cw[i] = own[i];
+        sw[i] = 0.f;
+        if (e < rot) {
+          const bool second = inter ? (e & 1) : e >= half;
+          const float2 cs = tab[warp][inter ? e >> 1 : second ? e - half : e];
+          const int pe = inter ? e ^ 1 : second ? e - half : e + half;
+          cw[i] *= cs.x;
+          sw[i] = (second ? cs.y : -cs.y) * (w ? Elem<T>::to_f(w[pe]) : 1.f);
         }
-        __syncwarp();  // q_out may be q: all partners are read before a row is stored
-      }
-      if (!is_v) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = e0 + i < rot ? fmaf(z[i], s[i], y[i] * c[i]) : y[i];
       }
     }
-    uint32_t top = 0;
-    if constexpr (SINK == kPoolE4m3) {
+    for (int pb = lo; pb < hi; pb += kBatch) {
+      uint4 raw[kBatch];
 #pragma unroll
-      for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = (pb + k) * RPW + sub;
+        raw[k] = pb + k < hi && r < rows ? *reinterpret_cast<const uint4*>(in + r * row_stride + e0)
+                                         : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + b * a.ob + t * a.ot + (int64_t)r * a.oh + e0) =
-          Pack<T, E>::pack(x);
-      continue;
-    }
-    const int h = r - a.Hq - (is_v ? a.Hkv : 0);
-    if constexpr (SINK == kDense) {
-      T* dst = static_cast<T*>(is_v ? a.V : a.K) + b * a.sb + h * a.sh + pos * a.st + e0;
-      *reinterpret_cast<uint4*>(dst) = Pack<T, E>::pack(x);
-    } else if (store) {
-      const int64_t row = ((blk * a.Hkv + h) << a.pool.shift) + (pos & (((int64_t)1 << a.pool.shift) - 1));
-      if constexpr (SINK == kPoolRaw) {
-        *reinterpret_cast<uint4*>(static_cast<T*>(is_v ? a.pool.V : a.pool.K) + row * D + e0) = Pack<T, E>::pack(x);
-      } else {
-        const int E8 = row_exponent(top);
-        // 2^-e, an fp32 normal over the whole of [-120, 119]: the product is exact (bf16 or fp32 x; tiny
-        // x below fp32's normals keep their bits, as the product is larger)
-        const float f = __uint_as_float((uint32_t)(254 - (E8 == 255 ? 127 : E8)) << 23);
-        uint32_t w[E / 4];
+      for (int k = 0; k < kBatch; ++k) {
+        if (pb + k >= hi) break;
+        const int r = (pb + k) * RPW + sub;
+        const bool live = r < rows;
+        float x[E];
+        Pack<T, E>::unpack(raw[k], x);
+        if (turned) {
+          float rstd = 1.f;
+          if (w) {
+            float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * f, x[4 * i + 1] * f), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi =
-              __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * f, x[4 * i + 3] * f), __NV_SATFINITE, __NV_E4M3);
-          w[i] = E8 == 255 ? 0x7f7f7f7fu : lo | (hi << 16);
+            for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rstd = rsqrtf(ss * (1.f / D) + a.rope.eps);
+          }
+          float z[E];
+          if (inter) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) z[i] = x[i ^ 1];
+          } else if (by_shuffle) {
+            uint4 o;
+            o.x = __shfl_sync(0xffffffffu, raw[k].x, src);
+            o.y = __shfl_sync(0xffffffffu, raw[k].y, src);
+            o.z = __shfl_sync(0xffffffffu, raw[k].z, src);
+            o.w = __shfl_sync(0xffffffffu, raw[k].w, src);
+            Pack<T, E>::unpack(o, z);
+          } else {
+            // a pair's channels at a distance no 16-byte word divides: the
+            // partners come from the row itself
+            const T* xr = in + (live ? r : rows - 1) * row_stride;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              const int e = e0 + i;
+              z[i] = e < rot ? Elem<T>::to_f(xr[e < half ? e + half : e - half]) : 0.f;
+            }
+            __syncwarp();  // q_out may be q: all partners are read before a row is stored
+          }
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            // (a channel that is not turned takes no partner: 0 times an infinity is NaN)
+            const float y = x[i] * cw[i];
+            x[i] = (e0 + i < rot ? fmaf(z[i], sw[i], y) : y) * rstd;
+          }
         }
-        uint8_t* dst = static_cast<uint8_t*>(is_v ? a.pool.V : a.pool.K) + row * D + e0;
-        if constexpr (E == 8)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else
-          *reinterpret_cast<uint32_t*>(dst) = w[0];
-        if (li == 0) (is_v ? a.pool.Ve : a.pool.Ke)[row] = (uint8_t)E8;
+        if (kind == 0) {
+          if (live)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + b * a.ob + t * a.ot + r * a.oh + e0) =
+                Pack<T, E>::pack(x);
+          continue;
+        }
+        if constexpr (SINK == kDense) {
+          if (live)
+            *reinterpret_cast<uint4*>(static_cast<T*>(kind == 2 ? a.V : a.K) + b * a.sb + r * a.sh + pos * a.st + e0) =
+                kind == 2 ? raw[k] : Pack<T, E>::pack(x);
+        } else {
+          const int64_t row = ((blk * a.Hkv + r) << a.pool.shift) + in_block;
+          if constexpr (SINK == kPoolRaw) {
+            if (live && store)
+              *reinterpret_cast<uint4*>(static_cast<T*>(kind == 2 ? a.pool.V : a.pool.K) + row * D + e0) =
+                  kind == 2 ? raw[k] : Pack<T, E>::pack(x);
+          } else {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int E8 = row_exponent(top);
+            // 2^-e, an fp32 normal over the whole of [-120, 119]: the product is exact (bf16 or fp32 x; tiny
+            // x below fp32's normals keep their bits, as the product is larger)
+            const float f = __uint_as_float((uint32_t)(254 - (E8 == 255 ? 127 : E8)) << 23);
+            uint32_t c[E / 4];
+#pragma unroll
+            for (int i = 0; i < E / 4; ++i) {
+              const uint32_t l2 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * f, x[4 * i + 1] * f), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t h2 =
+                  __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * f, x[4 * i + 3] * f), __NV_SATFINITE, __NV_E4M3);
+              c[i] = E8 == 255 ? 0x7f7f7f7fu : l2 | (h2 << 16);
+            }
+            if (live && store) {
+              uint8_t* dst = static_cast<uint8_t*>(kind == 2 ? a.pool.V : a.pool.K) + row * D + e0;
+              if constexpr (E == 8)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+              else
+                *reinterpret_cast<uint32_t*>(dst) = c[0];
+              if (li == 0) (kind == 2 ? a.pool.Ve : a.pool.Ke)[row] = (uint8_t)E8;
+            }
+          }
+        }
       }
     }
   }
@@ -294,42 +319,72 @@ __global__ void __launch_bounds__(128) pool_read_kernel(ReadArgs a) {
   const int c = threadIdx.x % PPR, r = threadIdx.x / PPR;
   const int64_t mask = ((int64_t)1 << a.pool.shift) - 1;
   const int32_t* table = a.batch.table + (int64_t)b * a.batch.max_blocks;
-#pragma unroll 4
-  for (int64_t t = t0 + r; t < t1; t += RPP) {
-    const int64_t blk = table[t >> a.pool.shift];
-    if (blk < 0 || blk >= a.pool.blocks) {
-      if (c == 0) set_status(a.status, LOD_ST_BAD_PAGE);
-      continue;
+  constexpr int PASSES = kReadTokens / RPP;  // rows of a thread
+  constexpr int BATCH = PASSES < 4 ? PASSES : 4;
+#pragma unroll 1
+  for (int p0 = 0; p0 < PASSES; p0 += BATCH) {
+    // the rows of a batch first, then all their loads, then the stores
+    int64_t row[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t t = t0 + r + (int64_t)(p0 + k) * RPP;
+      row[k] = -1;
+      if (t < t1) {
+        const int64_t blk = table[t >> a.pool.shift];
+        if (blk >= 0 && blk < a.pool.blocks)
+          row[k] = ((blk * a.pool.Hkv + h) << a.pool.shift) + (t & mask);
+        else if (c == 0)
+          set_status(a.status, LOD_ST_BAD_PAGE);
+      }
     }
-    const int64_t row = ((blk * a.pool.Hkv + h) << a.pool.shift) + (t & mask);
-    const int64_t dst = b * a.sb + h * a.sh + t * a.st + c * E;
+    uint4 x[BATCH][2];
+    int E8[BATCH][2];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const void* base = kv ? a.pool.V : a.pool.K;
-      T* out = static_cast<T*>(kv ? a.V : a.K) + dst;
-      if constexpr (!Q8) {
-        *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row * D + c * E);
-      } else {
-        const uint8_t* src = static_cast<const uint8_t*>(base) + row * D + c * E;
-        uint32_t w[E / 4];
-        if constexpr (E == 8) {
-          const uint2 x = *reinterpret_cast<const uint2*>(src);
-          w[0] = x.x;
-          w[1] = x.y;
+    for (int k = 0; k < BATCH; ++k) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (row[k] < 0) continue;
+        const void* base = kv ? a.pool.V : a.pool.K;
+        if constexpr (!Q8) {
+          x[k][kv] = *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + row[k] * D + c * E);
         } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(src);
+          const uint8_t* src = static_cast<const uint8_t*>(base) + row[k] * D + c * E;
+          E8[k][kv] = (kv ? a.pool.Ve : a.pool.Ke)[row[k]];
+          if constexpr (E == 8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src);
+            x[k][kv].x = w.x;
+            x[k][kv].y = w.y;
+          } else {
+            x[k][kv].x = *reinterpret_cast<const uint32_t*>(src);
+          }
         }
-        const int E8 = (kv ? a.pool.Ve : a.pool.Ke)[row];
-        const float f = E8 == 255 ? NAN : E8 == 0 ? __uint_as_float(0x400000u) : __uint_as_float((uint32_t)E8 << 23);
-        float x[E];
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-          const float2 v = __half22float2(__half2(hr));
-          x[2 * i] = v.x * f;
-          x[2 * i + 1] = v.y * f;
+    for (int k = 0; k < BATCH; ++k) {
+      if (row[k] < 0) continue;
+      const int64_t t = t0 + r + (int64_t)(p0 + k) * RPP;
+      const int64_t dst = b * a.sb + h * a.sh + t * a.st + c * E;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(kv ? a.V : a.K) + dst);
+        if constexpr (!Q8) {
+          *out = x[k][kv];
+        } else {
+          const int e = E8[k][kv];
+          const float f = e == 255 ? NAN : e == 0 ? __uint_as_float(0x400000u) : __uint_as_float((uint32_t)e << 23);
+          const uint32_t w[2] = {x[k][kv].x, x[k][kv].y};
+          float y[E];
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const __half2_raw hr =
+                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+            const float2 v = __half22float2(__half2(hr));
+            y[2 * i] = v.x * f;
+            y[2 * i + 1] = v.y * f;
+          }
+          *out = Pack<T, E>::pack(y);
         }
-        *reinterpret_cast<uint4*>(out) = Pack<T, E>::pack(x);
       }
     }
   }
@@ -353,7 +408,7 @@ cudaError_t launch_append_rows(const AppendArgs& args, int dtype, int d, bool po
   // one pass.
   const int elem = dtype == LOD_DTYPE_F32 ? 4 : 2;
   const int rpw = 32 / (d * elem / 16);
-  const int passes = (a.Hq + 2 * a.Hkv + rpw - 1) / rpw;
+  const int passes = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);
   int64_t split = (int64_t)148 * 16 / a.N;
   if (split > passes) split = passes;
   if (split < 1) split = 1;
