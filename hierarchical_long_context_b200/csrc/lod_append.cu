@@ -84,18 +84,23 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 
 // One warp per (token, share of its heads); a row of d channels is held by
 // LPR lanes, 16 bytes each, so a pass of the warp covers 32 / LPR rows (heads)
-// of the token, and kBatch passes' loads are in flight together.  The rows go
+// of the token, and the next kBatch passes' rows are loaded while those are
+// worked on.  The rows go
 // by kind (queries, keys, values).  For a kind, a channel's cosine is
 // multiplied by its norm weight and its sine by its partner's once, so that a
 // row takes out = rstd * (x * cw + partner * sw): the partners cross lanes as
 // the stored 16-byte words, not as floats.  Every row is read once and written
-// once (memory bound: 32768 tokens of 32 + 16 heads, 128 bf16 channels, take
-// the 805 MB in and out at the time the launch comment gives).
+// once.  32768 tokens of 32 + 16 heads, 128 bf16 channels (805 MB in and out):
+// 207 us, 59 % of the measured copy rate; without norm and rotation 178 us,
+// so the issue of about 75 instructions a pass and the latency at a token's
+// start bound it, not the bytes.  Measured and dropped: batches of 4 (220), 8
+// CTAs an SM (223), tokens in a loop over warps that keep their weights (230),
+// one flat loop over the passes of all kinds (258).
 template <typename T, int D, int SINK>
-__global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int E = 16 / (int)sizeof(T);
   constexpr int LPR = D / E, RPW = 32 / LPR;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 2;
   __shared__ float2 tab[4][kMaxPairs];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR, e0 = li * E;
@@ -180,14 +185,21 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const __grid_constant_
         }
       }
     }
-    for (int pb = lo; pb < hi; pb += kBatch) {
-      uint4 raw[kBatch];
+    uint4 ahead[kBatch];  // the next batch's rows: loaded while a batch is worked on
+    auto load = [&](int pb) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int r = (pb + k) * RPW + sub;
-        raw[k] = pb + k < hi && r < rows ? *reinterpret_cast<const uint4*>(in + r * row_stride + e0)
-                                         : make_uint4(0, 0, 0, 0);
+        ahead[k] = pb + k < hi && r < rows ? *reinterpret_cast<const uint4*>(in + r * row_stride + e0)
+                                           : make_uint4(0, 0, 0, 0);
       }
+    };
+    load(lo);
+    for (int pb = lo; pb < hi; pb += kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) raw[k] = ahead[k];
+      load(pb + kBatch);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (pb + k >= hi) break;
