@@ -15,18 +15,19 @@ namespace {
 // channels of O, so 16 neighbouring lanes own a row and its maximum and sum
 // need no shared memory.  fp32 has no tensor-core form of its own accuracy,
 // so FFMA bounds it; per 4 channels a thread reads RPT + 4 vectors for 16 RPT
-// FMAs.
+// FMAs (as pairs: fma.rn.f32x2).
 template <typename T, int D, int TM, bool Q8>
 __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAttendArgs a) {
   constexpr int KT = 64, NT = TM == 16 ? 128 : 256, RPT = TM * 16 / NT, CPT = D / 16;
   constexpr int KS = D + 4, PS = KT + 4;
   constexpr int E = 16 / (int)sizeof(T), PPR = D / E;
+  static_assert(E == 4, "fp32 rows");
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;               // [TM][D]
   float* Ks = Qs + TM * D;      // [KT][KS]
   float* Vs = Ks + KT * KS;     // [KT][D]
   float* Ps = Vs + KT * D;      // [TM][PS]
-  int* live = reinterpret_cast<int*>(Ps + TM * PS);  // [KT]: the key exists
+  int* live = reinterpret_cast<int*>(Ps + TM * PS);  // [2][KT]: the key exists (two tiles: they are loaded ahead)
   __shared__ int64_t wb_s[kInlineSeqs + 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
@@ -58,7 +59,8 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 #pragma unroll
       for (int i = 0; i < E; ++i) Qs[r * D + c * E + i] = v[i];
     }
-    float m[RPT], l[RPT], acc[RPT][CPT];
+    float m[RPT], l[RPT];
+    float2 acc[RPT][CPT / 2];
     int64_t pos[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -67,10 +69,12 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
       l[i] = 0.f;
       pos[i] = r < nrow ? s.len - s.n + (row0 + r) / a.G : -1;
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) acc[i][j] = 0.f;
+      for (int j = 0; j < CPT / 2; ++j) acc[i][j] = make_float2(0.f, 0.f);
     }
-    for (int kt = kt0; kt < kt1; ++kt) {
-      __syncthreads();
+    // One tile's keys (z = 0) or values (z = 1) to shared memory, as fp32.
+    // fp32 rows go by asynchronous copies: the next tile's keys while this
+    // tile's weights meet the values, its values during the next scores.
+    auto load_tile = [&](int kt, int z) {
       for (int x = tid; x < KT * PPR; x += NT) {
         const int k = x / PPR, c = x % PPR;
         const int64_t t = (int64_t)kt * KT + k;
@@ -82,63 +86,71 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
             set_status(a.status, LOD_ST_BAD_PAGE);
           }
         }
-        if (c == 0) live[k] = blk >= 0;
-        float kv[2][E];
+        if (z == 0 && c == 0) live[(kt & 1) * KT + k] = blk >= 0;
+        const int64_t row = ((blk * a.pool.Hkv + u.h) << a.pool.shift) + (t & (((int64_t)1 << a.pool.shift) - 1));
+        const void* base = z ? a.pool.V : a.pool.K;
+        float* to = z ? &Vs[k * D + c * E] : &Ks[k * KS + c * E];
+        if constexpr (!Q8) {
+          cp_async16_zfill(to, blk >= 0 ? static_cast<const T*>(base) + row * D + c * E : static_cast<const T*>(base),
+                           blk >= 0);
+        } else {
+          float v[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) kv[0][i] = kv[1][i] = 0.f;
-        if (blk >= 0) {
-          const int64_t row = ((blk * a.pool.Hkv + u.h) << a.pool.shift) + (t & (((int64_t)1 << a.pool.shift) - 1));
+          for (int i = 0; i < E; ++i) v[i] = 0.f;
+          if (blk >= 0) {
+            const uint8_t* src = static_cast<const uint8_t*>(base) + row * D + c * E;
+            const int E8 = (z ? a.pool.Ve : a.pool.Ke)[row];
+            const float f = E8 == 255 ? NAN : E8 == 0 ? __uint_as_float(0x400000u) : __uint_as_float((uint32_t)E8 << 23);
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(src);
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const void* base = z ? a.pool.V : a.pool.K;
-            if constexpr (!Q8) {
-              load_f<T, E>(static_cast<const T*>(base) + row * D + c * E, kv[z]);
-            } else {
-              const uint8_t* src = static_cast<const uint8_t*>(base) + row * D + c * E;
-              const int E8 = (z ? a.pool.Ve : a.pool.Ke)[row];
-              const float f = E8 == 255 ? NAN : E8 == 0 ? __uint_as_float(0x400000u) : __uint_as_float((uint32_t)E8 << 23);
-#pragma unroll
-              for (int i = 0; i < E / 4; ++i) {
-                const uint32_t word = reinterpret_cast<const uint32_t*>(src)[i];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const __half2_raw hr =
-                      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * j)), __NV_E4M3);
-                  const float2 f2 = __half22float2(__half2(hr));
-                  kv[z][4 * i + 2 * j] = f2.x * f;
-                  kv[z][4 * i + 2 * j + 1] = f2.y * f;
-                }
-              }
+            for (int j = 0; j < 2; ++j) {
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (16 * j)), __NV_E4M3);
+              const float2 f2 = __half22float2(__half2(hr));
+              v[2 * j] = f2.x * f;
+              v[2 * j + 1] = f2.y * f;
             }
           }
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          Ks[k * KS + c * E + i] = kv[0][i];
-          Vs[k * D + c * E + i] = kv[1][i];
+          *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
         }
       }
+      if constexpr (!Q8) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load_tile(kt0, 0);
+    load_tile(kt0, 1);
+    for (int kt = kt0; kt < kt1; ++kt) {
+      // this tile's keys (the values may still be on their way)
+      if constexpr (!Q8) asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
-      // S: rows ty * RPT + i, keys tx + 16 j
+      // S: rows ty * RPT + i, keys tx + 16 j, even and odd channels apart
       float sc[RPT][4];
-#pragma unroll
-      for (int i = 0; i < RPT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
-#pragma unroll 4
-      for (int e = 0; e < D; e += 4) {
-        float4 kk[4], qq[RPT];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * j) * KS + e]);
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) qq[i] = *reinterpret_cast<const float4*>(&Qs[(ty * RPT + i) * D + e]);
+      {
+        float2 s2[RPT][4];
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sc[i][j] = fmaf(qq[i].x, kk[j].x,
-                            fmaf(qq[i].y, kk[j].y, fmaf(qq[i].z, kk[j].z, fmaf(qq[i].w, kk[j].w, sc[i][j]))));
+          for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int e = 0; e < D; e += 4) {
+          float4 kk[4], qq[RPT];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * j) * KS + e]);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i) qq[i] = *reinterpret_cast<const float4*>(&Qs[(ty * RPT + i) * D + e]);
+#pragma unroll
+          for (int i = 0; i < RPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              s2[i][j] = ffma2(make_float2(qq[i].x, qq[i].y), make_float2(kk[j].x, kk[j].y), s2[i][j]);
+              s2[i][j] = ffma2(make_float2(qq[i].z, qq[i].w), make_float2(kk[j].z, kk[j].w), s2[i][j]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[i][j] = s2[i][j].x + s2[i][j].y;
       }
+      __syncthreads();  // the keys have been read
+      if (kt + 1 < kt1) load_tile(kt + 1, 0);
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
         float mx = -INFINITY;
@@ -146,7 +158,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
         for (int j = 0; j < 4; ++j) {
           const int k = tx + 16 * j;
           const int64_t t = (int64_t)kt * KT + k;
-          const bool seen = live[k] && t <= pos[i] && (a.window <= 0 || t > pos[i] - a.window);
+          const bool seen = live[(kt & 1) * KT + k] && t <= pos[i] && (a.window <= 0 || t > pos[i] - a.window);
           sc[i][j] = seen ? sc[i][j] * a.scale_log2 : -INFINITY;
           mx = fmaxf(mx, sc[i][j]);
         }
@@ -167,9 +179,14 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
         l[i] = fmaf(l[i], f, sum);
         m[i] = mn;
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) acc[i][j] *= f;
+        for (int j = 0; j < CPT / 2; ++j) acc[i][j] = make_float2(acc[i][j].x * f, acc[i][j].y * f);
       }
-      __syncwarp();  // a row's weights are written and read by one half warp
+      // this tile's values (the next keys may still be on their way)
+      if constexpr (!Q8) {
+        if (kt + 1 < kt1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      __syncthreads();
 #pragma unroll 2
       for (int k = 0; k < KT; k += 4) {
         float4 pp[RPT];
@@ -183,14 +200,14 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
               const float p = z == 0 ? pp[i].x : z == 1 ? pp[i].y : z == 2 ? pp[i].z : pp[i].w;
-              acc[i][4 * c + 0] = fmaf(p, vv.x, acc[i][4 * c + 0]);
-              acc[i][4 * c + 1] = fmaf(p, vv.y, acc[i][4 * c + 1]);
-              acc[i][4 * c + 2] = fmaf(p, vv.z, acc[i][4 * c + 2]);
-              acc[i][4 * c + 3] = fmaf(p, vv.w, acc[i][4 * c + 3]);
+              acc[i][2 * c] = ffma2(make_float2(p, p), make_float2(vv.x, vv.y), acc[i][2 * c]);
+              acc[i][2 * c + 1] = ffma2(make_float2(p, p), make_float2(vv.z, vv.w), acc[i][2 * c + 1]);
             }
           }
         }
       }
+      __syncthreads();  // the values have been read
+      if (kt + 1 < kt1) load_tile(kt + 1, 1);
     }
     // the unit's result, or this CTA's piece of it
     const bool whole = w.whole();
@@ -206,14 +223,17 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 #pragma unroll
         for (int c = 0; c < CPT / 4; ++c)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[c * 64 + tx * 4 + j] = Elem<T>::from_f(acc[i][4 * c + j] * inv);
+          for (int j = 0; j < 2; ++j) {
+            o[c * 64 + tx * 4 + 2 * j] = Elem<T>::from_f(acc[i][2 * c + j].x * inv);
+            o[c * 64 + tx * 4 + 2 * j + 1] = Elem<T>::from_f(acc[i][2 * c + j].y * inv);
+          }
         if (tx == 0 && a.lse) a.lse[tok * a.Hq + head] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
       } else {
         float* o = a.part + ((int64_t)slot * TM + r) * D;
 #pragma unroll
         for (int c = 0; c < CPT / 4; ++c)
           *reinterpret_cast<float4*>(o + c * 64 + tx * 4) =
-              make_float4(acc[i][4 * c], acc[i][4 * c + 1], acc[i][4 * c + 2], acc[i][4 * c + 3]);
+              make_float4(acc[i][2 * c].x, acc[i][2 * c].y, acc[i][2 * c + 1].x, acc[i][2 * c + 1].y);
         if (tx == 0) a.ml[(int64_t)slot * TM + r] = make_float2(m[i], l[i]);
       }
     }
@@ -223,7 +243,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 template <typename T, int D, int TM, bool Q8>
 cudaError_t launch_simt(const PoolAttendArgs& a, cudaStream_t st) {
   constexpr int KT = 64;
-  constexpr size_t smem = sizeof(float) * (TM * D + KT * (D + 4) + KT * D + TM * (KT + 4)) + sizeof(int) * KT;
+  constexpr size_t smem = sizeof(float) * (TM * D + KT * (D + 4) + KT * D + TM * (KT + 4)) + 2 * sizeof(int) * KT;
   cudaError_t e = set_smem_once<pool_simt_kernel<T, D, TM, Q8>>(smem);
   if (e == cudaSuccess && a.planned) e = launch_plan<TM, KT>(a, st);
   if (e != cudaSuccess) return e;
@@ -261,7 +281,7 @@ PoolShape pool_shape(int dtype, int bits, int d, int Hkv, int G, int B, int64_t 
   } else {
     s.TM = max_new * G <= 16 ? 16 : 64;
     s.KT = 64;
-    s.ctas = sms * 2;
+    s.ctas = s.TM == 64 && d == 128 ? sms : sms * 2;  // (CTAs an SM holds: 117 KB of shared memory, or 78 and less)
     s.inline_plan = max_new * G <= s.TM && B <= kInlineSeqs;
   }
   const int64_t tiles = N * G / s.TM + B;

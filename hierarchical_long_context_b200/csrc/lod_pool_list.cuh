@@ -112,12 +112,17 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
 // ---------------------------------------------------------------- merge
 
 // Joins the pieces of the unit whose first tile lies in part c of the list and
-// whose last lies behind it (there is at most one): pieces 2c + 1, 2(c + 1), 2(c + 2), ...
-// in that order, so the result does not depend on which CTA ran when.  One
-// warp per row, blockIdx.y picks 16 rows.
+// whose last lies behind it (there is at most one): pieces 2c + 1, 2(c + 1),
+// 2(c + 2), ..., summed in a fixed order, so the result does not depend on
+// which CTA ran when.  A CTA of 8 warps takes RB rows (blockIdx.y), 8 / RB
+// warps to a row that share its pieces (RB = 2), or two rows to a warp (16): a
+// unit of few rows is cut into many pieces, whose loads would follow one
+// another in a single warp (64 pieces of one row: 10 us).
 template <typename T, int D, int TM, int KT>
 __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
+  constexpr int RB = TM <= 16 ? 2 : 16, WPR = RB == 2 ? 4 : 1, C = D / 32;
   __shared__ int64_t wb_s[kInlineSeqs + 1];
+  __shared__ float sum_s[RB == 2 ? 8 : 1][D + 1];
   const int64_t* Wb = a.Wb;
   if (!a.planned) {
     plan_inline<TM, KT>(a, wb_s);
@@ -131,37 +136,56 @@ __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
   const int64_t uend = u.end();
   if (u.first() < w0 || u.first() >= w1 || uend <= w1) return;
   const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
-  const int64_t rows = (int64_t)s.n * a.G, row0 = u.i * TM;
-  const int nrow = rows - row0 < TM ? (int)(rows - row0) : TM;
+  const int rows = s.n * a.G, row0 = (int)u.i * TM;
+  const int nrow = rows - row0 < TM ? rows - row0 : TM;
+  if ((int)blockIdx.y * RB >= nrow) return;
   const int pieces = (int)((uend - 1) / share) - (int)blockIdx.x + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int C = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % WPR;
   auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
-  for (int r = blockIdx.y * 16 + warp; r < nrow && r < (int)blockIdx.y * 16 + 16; r += 8) {
+#pragma unroll 1
+  for (int k = warp / WPR; k < RB; k += 8 / WPR) {
+    const int r = blockIdx.y * RB + k;
+    if (RB != 2 && r >= nrow) break;  // (with RB = 2 every warp comes to the barriers)
+    const bool live = r < nrow;
     float m = -INFINITY;
-    bool bad = false;  // NaN goes through the maximum unseen
-    for (int i = lane; i < pieces; i += 32) {
-      const float x = a.ml[slot(i) * TM + r].x;
-      m = fmaxf(m, x);
-      bad |= x != x;
-    }
+    for (int i = lane; live && i < pieces; i += 32) m = fmaxf(m, a.ml[slot(i) * TM + r].x);
     m = warp_max(m);
-    if (__any_sync(0xffffffffu, bad)) m = NAN;
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, o[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) o[j] = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
+    for (int i = slice; live && i < pieces; i += WPR) {
       const int64_t at = slot(i) * TM + r;
       const float2 x = a.ml[at];
       const float f = exp2f(x.x - ref);
       l = fmaf(x.y, f, l);
       const float* p = a.part + at * D + lane * C;
+      float v[C];
+      if constexpr (C == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(p);
+        v[0] = w.x, v[1] = w.y;
+      }
 #pragma unroll
-      for (int j = 0; j < C; ++j) o[j] = fmaf(p[j], f, o[j]);
+      for (int j = 0; j < C; ++j) o[j] = fmaf(v[j], f, o[j]);
     }
-    const int64_t g = row0 + r, tok = s.r0 + g / a.G, head = u.h * a.G + g % a.G;
+    if constexpr (WPR > 1) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) sum_s[warp][lane * C + j] = o[j];
+      if (lane == 0) sum_s[warp][D] = l;
+      __syncthreads();
+      if (slice != 0 || !live) continue;
+      for (int q = 1; q < WPR; ++q) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) o[j] += sum_s[warp + q][lane * C + j];
+        l += sum_s[warp + q][D];
+      }
+    }
+    const int g = row0 + r, head = u.h * a.G + g % a.G;
+    const int64_t tok = s.r0 + g / a.G;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     T* out = static_cast<T*>(a.out) + tok * a.ot + head * a.oh + lane * C;
 #pragma unroll
@@ -178,7 +202,7 @@ cudaError_t launch_plan(const PoolAttendArgs& a, cudaStream_t st) {
 
 template <typename T, int D, int TM, int KT>
 cudaError_t launch_merge(const PoolAttendArgs& a, cudaStream_t st) {
-  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas * a.max_rounds, (TM + 15) / 16), 256, 0, st>>>(a);
+  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas * a.max_rounds, TM <= 16 ? TM / 2 : TM / 16), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
