@@ -95,6 +95,7 @@ struct PoolAttendArgs {
   int32_t* pre;            // [RT[B]] key tiles of the sequence (one head) before each row tile
   float* part;             // [parts][2][TM][d] partial sums
   float2* ml;              // [parts][2][TM] their (max, sum), log2 units
+  struct MergeRec* rec;    // [parts] the unit that opens in a part and goes on behind it
   int ctas;
   int min_share;           // key tiles a CTA takes at least
   int planned;             // 1: Wb, RT, pre were written by the plan kernel
@@ -180,6 +181,15 @@ __device__ __forceinline__ Unit find_unit(const PoolAttendArgs& a, const int64_t
   return u;
 }
 
+// What the merge needs of the unit whose first tile lies in a part and whose
+// last lies behind it (there is at most one): written by that part's CTA.
+// pieces = 0: there is none.
+struct __align__(16) MergeRec {
+  int pieces, nrow;  // parts it reaches into; its rows
+  int g0, head0;     // its first row, its first query head
+  int64_t r0;        // packed row of its sequence's first new token
+};
+
 // Parts of the list, and the entries of one.
 __device__ __forceinline__ int list_parts(const PoolAttendArgs& a) { return a.ctas * (a.rounds ? *a.rounds : 1); }
 __device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t total) {
@@ -240,6 +250,15 @@ struct Walk {
       row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
       piece();
     } while (kt0 == kt1);
+  }
+  // (after the walk; by one thread)
+  __device__ __forceinline__ void record(const int64_t* Wb, int part) const {
+    MergeRec r = {0, 0, 0, 0, 0};
+    if (w0 < w1 && uend > w1 && u.first() >= w0 && u.first() < w1) {
+      const int64_t share = list_share(a, Wb[a.batch.B]);
+      r = {(int)((uend - 1) / share) - part + 1, nrow, (int)u.i * TM, u.h * a.G, s.r0};
+    }
+    a.rec[part] = r;
   }
   __device__ __forceinline__ bool whole() const { return w <= u.first() && pe == uend; }
   __device__ __forceinline__ int slot(int part) const { return 2 * part + (u.first() >= w0 ? 1 : 0); }
@@ -309,7 +328,7 @@ struct PoolShape {
   int TM, KT, ctas;
   bool inline_plan;
   int max_rounds;
-  size_t off_plan, off_ml, off_part, total;  // workspace offsets
+  size_t off_plan, off_ml, off_rec, off_part, total;  // workspace offsets
 };
 // Stored bytes of a key and its value.
 inline int pool_row_bytes(int dtype, int bits, int d) {

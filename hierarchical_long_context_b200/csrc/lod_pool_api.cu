@@ -302,6 +302,7 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
     if (s.kind == 1) a.rounds = reinterpret_cast<int32_t*>(w + s.off_ml) - 4;  // the plan's last 16 bytes
   }
   a.ml = reinterpret_cast<float2*>(w + s.off_ml);
+  a.rec = reinterpret_cast<lod::MergeRec*>(w + s.off_rec);
   a.part = reinterpret_cast<float*>(w + s.off_part);
   a.ctas = s.ctas;
   a.max_rounds = s.max_rounds;

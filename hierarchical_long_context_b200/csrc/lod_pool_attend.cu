@@ -31,13 +31,16 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
   __shared__ int64_t wb_s[kInlineSeqs + 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
+  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
   const int64_t* Wb = a.Wb;
+  if (a.planned) pdl_wait();  // (the plan)
   if (!a.planned) {
     plan_inline<TM, KT>(a, wb_s);
     Wb = wb_s;
   }
   clear_refused<T, D>(a);
-  for (Walk<TM, KT> w(a, Wb, blockIdx.x); w.more(); w.next()) {
+  Walk<TM, KT> w(a, Wb, blockIdx.x);
+  for (; w.more(); w.next()) {
     const Unit& u = w.u;
     const SeqView& s = w.s;
     const int kt0 = w.kt0, kt1 = w.kt1, nrow = w.nrow;
@@ -238,6 +241,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
       }
     }
   }
+  if (tid == 0) w.record(Wb, blockIdx.x);
 }
 
 template <typename T, int D, int TM, bool Q8>
@@ -247,8 +251,13 @@ cudaError_t launch_simt(const PoolAttendArgs& a, cudaStream_t st) {
   cudaError_t e = set_smem_once<pool_simt_kernel<T, D, TM, Q8>>(smem);
   if (e == cudaSuccess && a.planned) e = launch_plan<TM, KT>(a, st);
   if (e != cudaSuccess) return e;
-  pool_simt_kernel<T, D, TM, Q8><<<a.ctas, TM == 16 ? 128 : 256, smem, st>>>(a);
-  e = cudaGetLastError();
+  const dim3 grid(a.ctas), block(TM == 16 ? 128 : 256);
+  if (a.planned) {
+    e = launch_pdl(pool_simt_kernel<T, D, TM, Q8>, grid, block, smem, st, a);
+  } else {
+    pool_simt_kernel<T, D, TM, Q8><<<grid, block, smem, st>>>(a);
+    e = cudaGetLastError();
+  }
   return e != cudaSuccess ? e : launch_merge<T, D, TM, KT>(a, st);
 }
 
@@ -289,7 +298,8 @@ PoolShape pool_shape(int dtype, int bits, int d, int Hkv, int G, int B, int64_t 
   s.off_plan = kWsHeader;
   size_t plan = s.inline_plan ? 0 : (size_t)(B + 1) * 16 + (size_t)tiles * 4 + 16;
   s.off_ml = s.off_plan + up(plan);
-  s.off_part = s.off_ml + up((size_t)s.ctas * s.max_rounds * 2 * s.TM * sizeof(float2));
+  s.off_rec = s.off_ml + up((size_t)s.ctas * s.max_rounds * 2 * s.TM * sizeof(float2));
+  s.off_part = s.off_rec + up((size_t)s.ctas * s.max_rounds * sizeof(MergeRec));
   s.total = s.off_part + up((size_t)s.ctas * s.max_rounds * 2 * s.TM * d * sizeof(float));
   return s;
 }

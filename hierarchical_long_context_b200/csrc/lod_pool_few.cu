@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   for (int i = tid; i < 2 * S::kP / 16; i += blockDim.x)  // rows of P past RQ stay zero
     reinterpret_cast<uint4*>(sm + S::off_P)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async();
+  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
   const int64_t* Wb = a.Wb;
+  if (a.planned) pdl_wait();  // (the plan)
   if (!a.planned) {
     plan_inline<RQ, kKT>(a, wb_s);
     Wb = wb_s;
@@ -332,7 +334,8 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     int2* pos = pos_s + half * 64;
     int c0 = 0, k = 0;  // the unit's first tile, units
     bool go = true;
-    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more(); w.next(), ++k) {
+    Walk<RQ, kKT> w(a, Wb, blockIdx.x);
+    for (; w.more(); w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
       const float* qe = qe_s + (k & 15) * NQ;
       float cv = 0.f;  // (8-bit) a value exponent of the unit: sums of weights are in units of 2^cv
@@ -532,6 +535,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       bar_named_sync(kBarBoth, 256);  // both O^T, fin_s and up_s have been read
       c0 += T;
     }
+    if (half == 0 && r == 0) w.record(Wb, blockIdx.x);
   } else if constexpr (Q8) {
     // ============================================================== codes to f16 tiles
     regs_dec<64>();
@@ -573,8 +577,13 @@ cudaError_t launch_few(const PoolAttendArgs& a, const PoolMaps* maps, cudaStream
   if (e == cudaSuccess && a.planned) e = launch_plan<RQ, kKT>(a, st);
   if (e != cudaSuccess) return e;
   PoolMaps none = {};
-  pool_few_kernel<D, RQ, Q8><<<a.ctas, Q8 ? 640 : 384, S::bytes, st>>>(maps ? *maps : none, a);
-  e = cudaGetLastError();
+  const dim3 grid(a.ctas), block(Q8 ? 640 : 384);
+  if (a.planned) {
+    e = launch_pdl(pool_few_kernel<D, RQ, Q8>, grid, block, S::bytes, st, maps ? *maps : none, a);
+  } else {
+    pool_few_kernel<D, RQ, Q8><<<grid, block, S::bytes, st>>>(maps ? *maps : none, a);
+    e = cudaGetLastError();
+  }
   return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, RQ, kKT>(a, st);
 }
 

@@ -40,6 +40,7 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
 // a warp per sequence for the sums inside it.
 template <int TM, int KT>
 __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
+  pdl_launch_dependents();
   __shared__ int64_t ws[32];
   const int B = a.batch.B, lane = threadIdx.x & 31;
   int64_t at = 0, total;
@@ -121,25 +122,12 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
 template <typename T, int D, int TM, int KT>
 __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
   constexpr int RB = TM <= 16 ? 2 : 16, WPR = RB == 2 ? 4 : 1, C = D / 32;
-  __shared__ int64_t wb_s[kInlineSeqs + 1];
   __shared__ float sum_s[RB == 2 ? 8 : 1][D + 1];
-  const int64_t* Wb = a.Wb;
-  if (!a.planned) {
-    plan_inline<TM, KT>(a, wb_s);
-    Wb = wb_s;
-  }
+  pdl_wait();
   if ((int)blockIdx.x >= list_parts(a)) return;
-  const int64_t total = Wb[a.batch.B], share = list_share(a, total);
-  const int64_t w0 = blockIdx.x * share, w1 = w0 + share;
-  if (w1 >= total) return;
-  const Unit u = find_unit<TM, KT>(a, Wb, w1 - 1);
-  const int64_t uend = u.end();
-  if (u.first() < w0 || u.first() >= w1 || uend <= w1) return;
-  const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
-  const int rows = s.n * a.G, row0 = (int)u.i * TM;
-  const int nrow = rows - row0 < TM ? rows - row0 : TM;
-  if ((int)blockIdx.y * RB >= nrow) return;
-  const int pieces = (int)((uend - 1) / share) - (int)blockIdx.x + 1;
+  const MergeRec u = a.rec[blockIdx.x];
+  const int nrow = u.nrow, pieces = u.pieces;
+  if (pieces == 0 || (int)blockIdx.y * RB >= nrow) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % WPR;
   auto slot = [&](int i) -> int64_t { return 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0); };
 #pragma unroll 1
@@ -184,8 +172,8 @@ __global__ void __launch_bounds__(256) pool_merge_kernel(PoolAttendArgs a) {
         l += sum_s[warp + q][D];
       }
     }
-    const int g = row0 + r, head = u.h * a.G + g % a.G;
-    const int64_t tok = s.r0 + g / a.G;
+    const int g = u.g0 + r, head = u.head0 + g % a.G;
+    const int64_t tok = u.r0 + g / a.G;
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     T* out = static_cast<T*>(a.out) + tok * a.ot + head * a.oh + lane * C;
 #pragma unroll
@@ -202,8 +190,8 @@ cudaError_t launch_plan(const PoolAttendArgs& a, cudaStream_t st) {
 
 template <typename T, int D, int TM, int KT>
 cudaError_t launch_merge(const PoolAttendArgs& a, cudaStream_t st) {
-  pool_merge_kernel<T, D, TM, KT><<<dim3(a.ctas * a.max_rounds, TM <= 16 ? TM / 2 : TM / 16), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(pool_merge_kernel<T, D, TM, KT>, dim3(a.ctas * a.max_rounds, TM <= 16 ? TM / 2 : TM / 16), dim3(256),
+                    0, st, a);
 }
 
 }  // namespace

@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     }
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
+  pdl_wait();               // (the plan)
   clear_refused<__nv_bfloat16, D>(a);
   tc::fence_before_sync();
   __syncthreads();
@@ -276,8 +278,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     uint32_t ns = 0, no = 0;  // key halves and outputs taken
     int c = 0;                // ring position of the next key tile's K
     bool go = true;
-    for (int part = blockIdx.x; part < parts && go; part += a.ctas)
-      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
+    for (int part = blockIdx.x; part < parts && go; part += a.ctas) {
+      Walk<kTM, kKT> w(a, a.Wb, part);
+      for (; w.more() && go; w.next()) {
       const int T = w.kt1 - w.kt0;
       if (s * 128 >= w.nrow) {
         c += 2 * T;
@@ -480,6 +483,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         else if (a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
       }
       tc::fence_before_sync();  // O_s is read before the next unit's weights are announced
+      }
+      if (s == 0 && r == 0) w.record(a.Wb, part);
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to bf16 tiles
@@ -518,8 +523,7 @@ cudaError_t launch_rows(const PoolAttendArgs& a, const PoolMaps* maps, cudaStrea
   if (e == cudaSuccess) e = launch_plan<kTM, kKT>(a, st);
   if (e != cudaSuccess) return e;
   PoolMaps none = {};
-  pool_rows_kernel<D, Q8><<<a.ctas, Q8 ? 512 : 384, RowsSmem<D, Q8>::bytes, st>>>(maps ? *maps : none, a);
-  e = cudaGetLastError();
+  e = launch_pdl(pool_rows_kernel<D, Q8>, dim3(a.ctas), dim3(Q8 ? 512 : 384), RowsSmem<D, Q8>::bytes, st, maps ? *maps : none, a);
   return e != cudaSuccess ? e : launch_merge<__nv_bfloat16, D, kTM, kKT>(a, st);
 }
 
