@@ -31,7 +31,6 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
   __shared__ int64_t wb_s[kInlineSeqs + 1];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
-  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
   const int64_t* Wb = a.Wb;
   if (a.planned) pdl_wait();  // (the plan)
   if (!a.planned) {

@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   for (int i = tid; i < 2 * S::kP / 16; i += blockDim.x)  // rows of P past RQ stay zero
     reinterpret_cast<uint4*>(sm + S::off_P)[i] = make_uint4(0, 0, 0, 0);
   tc::fence_proxy_async();
-  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
   const int64_t* Wb = a.Wb;
   if (a.planned) pdl_wait();  // (the plan)
   if (!a.planned) {
@@ -217,7 +216,8 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       const uint32_t qb = smem_u32(sm + S::off_Q), kb = smem_u32(sm + S::off_K);
       int c = 0, k = 0;  // key tiles, units
       bool go = true;
-      for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more() && go; w.next(), ++k) {
+      Walk<RQ, kKT> w(a, Wb, blockIdx.x);
+      for (; w.more() && go; w.next(), ++k) {
         if (!(go = __all_sync(0xffffffffu, wait_ring(q_full, 2, k)))) break;
         const uint64_t qd = tc::desc_kmajor_sw128(qb + (uint32_t)(k & 1) * S::kQ);
         const int T = w.kt1 - w.kt0;
@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           if (j == T - 1) mma_commit_if(lead, &q_empty[k & 1]);
         }
       }
+      if (lane == 0) w.record(Wb, blockIdx.x);
       if (c > 0) {
         mma_commit_if(lead, &fin[0]);
         (void)mbar_wait(&fin[0], 0, a.status);
@@ -334,8 +335,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     int2* pos = pos_s + half * 64;
     int c0 = 0, k = 0;  // the unit's first tile, units
     bool go = true;
-    Walk<RQ, kKT> w(a, Wb, blockIdx.x);
-    for (; w.more(); w.next(), ++k) {
+    for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more(); w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
       const float* qe = qe_s + (k & 15) * NQ;
       float cv = 0.f;  // (8-bit) a value exponent of the unit: sums of weights are in units of 2^cv
@@ -535,7 +535,6 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       bar_named_sync(kBarBoth, 256);  // both O^T, fin_s and up_s have been read
       c0 += T;
     }
-    if (half == 0 && r == 0) w.record(Wb, blockIdx.x);
   } else if constexpr (Q8) {
     // ============================================================== codes to f16 tiles
     regs_dec<64>();

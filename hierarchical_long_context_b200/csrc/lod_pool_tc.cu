@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     }
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
-  pdl_launch_dependents();  // (the merge; it waits for this grid's end)
   pdl_wait();               // (the plan)
   clear_refused<__nv_bfloat16, D>(a);
   tc::fence_before_sync();
@@ -192,8 +191,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         mma_commit_if(lead, &s_full[2 * s + u]);
         any = true;
       };
-      for (int part = blockIdx.x; part < parts && go; part += a.ctas)
-      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
+      for (int part = blockIdx.x; part < parts && go; part += a.ctas) {
+        Walk<kTM, kKT> w(a, a.Wb, part);
+        for (; w.more() && go; w.next()) {
         const int T = w.kt1 - w.kt0;
         if (s * 128 >= w.nrow) {  // no second query tile: its share of the ring is given back as it fills
           for (int j = 0; j < 2 * T && go; ++j, ++c) {
@@ -231,6 +231,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             }
           }
         }
+      }
+        if (s == 0 && lane == 0) w.record(a.Wb, part);
       }
       if (any) {
         mma_commit_if(lead, &fin[s]);
@@ -278,9 +280,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
     uint32_t ns = 0, no = 0;  // key halves and outputs taken
     int c = 0;                // ring position of the next key tile's K
     bool go = true;
-    for (int part = blockIdx.x; part < parts && go; part += a.ctas) {
-      Walk<kTM, kKT> w(a, a.Wb, part);
-      for (; w.more() && go; w.next()) {
+    for (int part = blockIdx.x; part < parts && go; part += a.ctas)
+      for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
       const int T = w.kt1 - w.kt0;
       if (s * 128 >= w.nrow) {
         c += 2 * T;
@@ -483,8 +484,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         else if (a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
       }
       tc::fence_before_sync();  // O_s is read before the next unit's weights are announced
-      }
-      if (s == 0 && r == 0) w.record(a.Wb, part);
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to bf16 tiles
