@@ -32,7 +32,7 @@ struct FewSmem {
   static constexpr size_t off_pos = off_qe + (Q8 ? 16 * 4 * NQ : 0);  // int2 [2][64]
   static constexpr size_t off_info = off_pos + 2 * 8 * 64;                          // uint32 [16]
   static constexpr size_t off_wb = off_info + 64;                               // int64 [kInlineSeqs + 1]
-  static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 2;
+  static constexpr int kBars = 2 * KS + 2 * VS + 2 * 2 * RS + 2 + 2 + 2 + 2 + 4 + 16 + 2;
   static constexpr size_t off_bar = off_wb + 8 * (kInlineSeqs + 1);
   static constexpr size_t bytes = off_bar + 8 * kBars + 48 + 1024;  // (TMEM slot, abort flag, scales)
   static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
@@ -61,8 +61,12 @@ struct FewSmem {
 // loads, exponentials and stores measured 1600 to 3000 cycles, more than its
 // bytes take, so two chains run side by side and are joined at the unit's
 // end), with an 8-bit pool warps 12-15 and 16-19 codes to f16 (keys, values).
-// Bound by the cache's bytes: 64 KB a tile (bf16, d = 128) at 1/148 of the
-// HBM rate is 1.5 us, the tensor work of a tile well below a tenth of that.
+// Bounds: the cache's bytes, 64 KB a tile (bf16, d = 128) at 1/148 of the HBM
+// rate, 1.5 us; the tensor work is below a tenth of that.  Measured at 4 x 64K
+// tokens, 64 / 8 heads, one new token: bf16 169 us (6.36 TB/s, 97 % of the
+// measured copy rate), d = 64 100 us (5.37 TB/s), four new tokens 198 us.
+// 8-bit: 140 us (3.8 TB/s).  There shared memory is the bound: codes in and
+// out, f16 tiles in and out of it are 192 KB a tile, 1500 cycles.
 template <int D, int RQ, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {
@@ -85,7 +89,8 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   uint64_t* pv_done = p_ready + 2;
   uint64_t* q_full = pv_done + 2;
   uint64_t* q_empty = q_full + 2;
-  uint64_t* fin = q_empty + 2;  // [2]
+  uint64_t* ex_full = q_empty + 2;  // [16] a tile's block mask and exponent bytes
+  uint64_t* fin = ex_full + 16;     // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
   volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* m_s = reinterpret_cast<float*>(sm + S::off_m);
@@ -121,6 +126,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&fin[i], 1);
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&ex_full[i], Q8 ? 33 : 1);
     *abort_s = 0;
     fence_mbar_init();
     if (!Q8) {
@@ -153,15 +159,15 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   const uint32_t all_ok = (per_tile == 32 ? 0xffffffffu : (1u << per_tile) - 1);
 
   // The copies of a unit's keys (kv = 0) or values (kv = 1); `c` counts key
-  // tiles.  The values' warp also leaves each tile's block mask before it
-  // announces the copy: the softmax waits for that one.  An 8-bit pool's
-  // exponent bytes go with the codes, to a ring of their own (the codes'
-  // stage is free again before the softmax has used them).
+  // tiles.  The values' warp also gives the softmax each tile's block mask and,
+  // of an 8-bit pool, the exponent bytes of keys and values (one 16-byte copy
+  // of 16 lanes; as bulk copies of a block's bytes they took as long to issue
+  // as the codes), with a barrier of their own: the softmax then starts on
+  // scores while the tile's values are still being converted.
   auto copies = [&](const Walk<RQ, kKT>& w, int kv, int& c) -> bool {
     Feed f(a, w.u.b, w.s.len, w.kt0, w.kt1);
     const int n = Q8 ? RS : kv ? VS : KS;
     const uint8_t* codes = static_cast<const uint8_t*>(kv ? a.pool.V : a.pool.K);
-    const uint8_t* exps = kv ? a.pool.Ve : a.pool.Ke;
     const CUtensorMap* map = kv ? &maps.V : &maps.K;
     const int Hkv = a.pool.Hkv, h = w.u.h;
     for (int kt = w.kt0; kt < w.kt1; f.advance(), ++kt, ++c) {
@@ -172,9 +178,25 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       uint64_t* full = Q8 ? &raw_full[st * 2 + kv] : (kv ? vfull : kfull) + st;
       if (c >= n && !wait(Q8 ? &raw_empty[st * 2 + kv] : (kv ? vempty : kempty) + st, (uint32_t)(c / n - 1) & 1u))
         return false;
+      if (kv == 1) {
+        if constexpr (Q8) {
+          const int x = (lane & 7) * 16;
+          const int e = __shfl_sync(0xffffffffu, f.cur, x >> shift);
+          if (lane < 16) {
+            const uint8_t* from = (lane < 8 ? a.pool.Ke : a.pool.Ve);
+            const bool there = e >= 0;
+            cp_async16_zfill(ex_s + (c & 15) * 256 + lane * 16,
+                             there ? from + (((int64_t)e * Hkv + h) << shift) + (x & ((1 << shift) - 1)) : from, there);
+          }
+          cp_async_mbar_arrive_noinc(&ex_full[c & 15]);
+        }
+        if (lane == 0) {
+          info_s[c & 15] = ok;
+          mbar_arrive(&ex_full[c & 15]);
+        }
+      }
       if (lane == 0) {
-        if (kv == 1) info_s[c & 15] = ok;
-        if (rows) mbar_arrive_expect(full, (uint32_t)rows * (Q8 ? D + 1 : 2 * D));
+        if (rows) mbar_arrive_expect(full, (uint32_t)rows * D * (Q8 ? 1 : 2));
         else mbar_arrive(full);
       }
       __syncwarp();
@@ -182,7 +204,6 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         if constexpr (Q8) {
           bulk_g2s(sm + S::off_raw + (st * 2 + kv) * S::kRaw + (lane << shift) * D, codes + (int64_t)row * D,
                    (uint32_t)D << shift, full);
-          bulk_g2s(ex_s + (c & 15) * 256 + kv * 128 + (lane << shift), exps + row, 1u << shift, full);
         } else {
           unsigned char* d = sm + (kv ? S::off_V : S::off_K) + (size_t)st * S::kTile + (lane << shift) * 128;
           tma_load_box(d, map, 0, row, full);
@@ -194,6 +215,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   };
   // after a wait has given up: copies still in flight land before the CTA ends
   auto drain = [&](int kv, int c) {
+    if (Q8) cp_async_wait_all();
     __syncwarp();
     if (!*abort_s || lane != 0) return;
     const int n = Q8 ? RS : kv ? VS : KS;
@@ -355,11 +377,10 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       const int j0 = (c0 ^ half) & 1;  // this warpgroup's first tile of the unit
       for (int j = j0; j < T; j += 2) {
         const int c = c0 + j, k0 = (w.kt0 + j) * kKT, t = k0 + r;
-        // (a barrier's parity tells a phase only from the one before it: with
-        // the sums of tile c - 2 complete, V_{c - VS} has landed)
-        static_assert(VS >= 2, "wait for the values");
-        go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(vfull, VS, c) &&
-                                         wait_ring(s_full, 2, c));
+        // (8-bit: the values too.  Conversion and softmax then take turns at the
+        // shared memory, which bounds both; side by side they measured 6 % more.)
+        go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(ex_full, 16, c) &&
+                                         (!Q8 || wait_ring(vfull, VS, c)) && wait_ring(s_full, 2, c));
         // (a failed wait is carried to the barrier below, where the four warps leave together)
         const uint32_t ok = info_s[c & 15];
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
@@ -373,6 +394,10 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         }
         if (masked) {
           live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
+          // (a barrier's parity tells a phase only from the one before it: with
+          // the sums of tile c - 2 complete, V_{c - VS} has landed)
+          static_assert(VS >= 2, "wait for the values");
+          go = go && __all_sync(0xffffffffu, wait_ring(vfull, VS, c));
           if (go && (!live || t < first_lo)) {
             // no row's key: the weights' zeros must not meet what the pool
             // holds there, or what shared memory held before

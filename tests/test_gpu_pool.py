@@ -583,6 +583,32 @@ def test_long_sequence_offsets_pass_32_bits():
     assert torch.equal(Kd[0, :, -9:], k.transpose(0, 1)) and torch.equal(Vd, Kd)
 
 
+@pytest.mark.parametrize("bits, window", [(0, 0), (8, 0), (0, 9000)])
+def test_a_cache_beyond_l2_is_taken_in_rounds(bits, window):
+    """164 MB of bf16 cache and more than 64 key tiles a CTA and round: the work list is walked in several rounds.
+    Some heads against the 64-bit form, all of them against calls of fewer rows."""
+    L, n = 40000, 2048
+    pool, table = make_pool(gen(60), [L], 64, 16, 8, 128, BF, bits)
+    begin, batch, q, out, lse, ws = run_attend(pool, table, [L], [n], 61, window=window)
+    assert lod.lod_get_status(ws) == 0
+    for h in (0, 7):  # KV heads, as pools of one head
+        cut = [None if x is None else x[:, h:h + 1].contiguous() for x in (pool.K, pool.V, pool.Ke, pool.Ve)]
+        one = api.Pool(*cut, Hq=2, dtype=BF)
+        for lo in (0, n - 40):
+            Lr = L - n + lo + 40
+            o, z, to, tz = pt.attend64(one, table, [Lr], [0, 40], q[lo:lo + 40, 2 * h:2 * h + 2], window)
+            close(out[lo:lo + 40, 2 * h:2 * h + 2], o, to, "out")
+            close(lse[lo:lo + 40, 2 * h:2 * h + 2], z, tz, "lse")
+    for lo, m in ((0, 100), (1000, 77)):  # another cut of the same rows: other partial sums, so bounds and not bits
+        b2 = api.PoolBatch(table, torch.tensor([L - n + lo + m], device="cuda"), torch.tensor([0, m], device="cuda"),
+                           tokens=m, max_new=m)
+        z2 = torch.zeros(m, 16, device="cuda")
+        o2 = lod.lod_pool_attend(pool, b2, q[lo:lo + m], lse=z2, window=window)
+        # both within 2^-8 (weights) of sum p |v| <= max |v| < 6, and 2^-8 of themselves
+        assert (o2.float() - out[lo:lo + m].float()).abs().max() < 2 * 6 * 2.0 ** -8
+        assert (z2 - lse[lo:lo + m]).abs().max() < 1e-4
+
+
 # ------------------------------------------------------------------ a run of them together
 
 @pytest.mark.parametrize("bits", [0, 8])
