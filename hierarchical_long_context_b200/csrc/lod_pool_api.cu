@@ -80,6 +80,11 @@ int32_t check_new_rows(const lod_pool* p, const lod_batch* b) {
     return fail(LOD_EINVAL, "batch N = %lld must be >= 1, with N * Hq below 2^31", (long long)b->N);
   if (b->max_new < 1 || b->max_new > b->N)
     return fail(LOD_EINVAL, "batch max_new = %lld must be in [1, N]", (long long)b->max_new);
+  // the attention's list counts a sequence's tiles in 32 bits (8 query rows, 64 keys and more a tile)
+  const int64_t row_tiles = b->max_new * (p->Hq / p->Hkv) / 8 + 1, key_tiles = (int64_t)b->max_blocks * p->block / 64 + 8;
+  if (row_tiles > (((int64_t)1 << 31) - 1) / key_tiles)
+    return fail(LOD_EUNSUPPORTED, "max_new = %lld rows over %lld tokens: too many tiles for one call",
+                (long long)b->max_new, (long long)b->max_blocks * p->block);
   return LOD_OK;
 }
 

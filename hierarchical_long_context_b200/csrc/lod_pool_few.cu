@@ -65,8 +65,10 @@ struct FewSmem {
 // rate, 1.5 us; the tensor work is below a tenth of that.  Measured at 4 x 64K
 // tokens, 64 / 8 heads, one new token: bf16 169 us (6.36 TB/s, 97 % of the
 // measured copy rate), d = 64 100 us (5.37 TB/s), four new tokens 198 us.
-// 8-bit: 140 us (3.8 TB/s).  There shared memory is the bound: codes in and
-// out, f16 tiles in and out of it are 192 KB a tile, 1500 cycles.
+// 8-bit: 140 us (3.8 TB/s).  There the codes and f16 tiles that go in and out
+// of shared memory, 192 KB a tile, take 1500 cycles of it (the load and store
+// instructions' part reads 31 % of that pipe), against 1400 for the bytes from
+// HBM, and the conversion and softmax chains share the rest.
 template <int D, int RQ, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     pool_few_kernel(const __grid_constant__ PoolMaps maps, const __grid_constant__ PoolAttendArgs a) {

@@ -75,6 +75,15 @@ def test_bad_batches_are_refused(kw):
     assert rc == _lib.LOD_EINVAL and "batch" in err()
 
 
+def test_calls_of_too_many_tiles_are_refused():
+    n = ctypes.c_size_t()
+    big = batch(B=1, max_blocks=1 << 26, N=1 << 22, max_new=1 << 22)
+    rc = _lib.load().lod_pool_workspace_bytes(ctypes.byref(pool()), ctypes.byref(big), ctypes.byref(n))
+    assert rc == _lib.LOD_EUNSUPPORTED and "tiles" in err()
+    long = batch(B=1, max_blocks=1 << 16, N=1 << 17, max_new=1 << 15)   # 32K new tokens of a 1M-token sequence
+    assert _lib.load().lod_pool_workspace_bytes(ctypes.byref(pool()), ctypes.byref(long), ctypes.byref(n)) == 0
+
+
 def test_workspace_bytes_need_no_pointers_and_grow():
     n, m = ctypes.c_size_t(), ctypes.c_size_t()
     L = _lib.load()
