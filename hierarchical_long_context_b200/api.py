@@ -54,6 +54,9 @@ class Params:
             object.__setattr__(self, "_ref", r)
         return r
 
+    def __getstate__(self):  # (copies and pickles leave the reference behind)
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
     @property
     def page_slots(self) -> int:
         return self.chunk // self.page + self.clusters

@@ -162,6 +162,15 @@ def test_unsupported_sizes_of_append_are_refused():
 
 # ---- the Python binding's own checks
 
+def test_params_with_a_kept_struct_copy_and_pickle():
+    import copy
+    import pickle
+    p = lod.Params(B=2, Hq=16, Hkv=4, d=128, Tmax=4096)
+    assert p.ref() is p.ref()
+    for q in (copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert q == p and q.ref() is not p.ref()
+
+
 def _cpu_pool(bits=0, **kw):
     return api.Pool.empty(8, 16, 4, 2, 64, bits=bits, device="cpu", **kw)
 
