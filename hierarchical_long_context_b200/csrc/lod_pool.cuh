@@ -325,7 +325,7 @@ cudaError_t launch_pool_read(const ReadArgs& a, int dtype, int bits, int d, cuda
 // Shape of an attention call: which kernel, its tiles and its CTAs.
 struct PoolShape {
   int kind;  // 0: CUDA cores (fp32); 1: tensor cores, 256 rows a unit; 2: tensor cores, few rows
-  int TM, KT, ctas;
+  int TM, ctas;
   bool inline_plan;
   int max_rounds;
   size_t off_plan, off_ml, off_rec, off_part, total;  // workspace offsets

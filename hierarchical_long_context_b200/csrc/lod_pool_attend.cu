@@ -10,15 +10,20 @@ namespace {
 // ---------------------------------------------------------------- CUDA cores
 
 // fp32 attention on the CUDA cores.  A CTA of 4 * TM threads (128 at least)
-// holds a tile of TM query rows; per 64-key tile S = Q K^T and O += P V from
-// shared memory, each thread RPT rows x 4 keys of S and the same rows x D/16
-// channels of O, so 16 neighbouring lanes own a row and its maximum and sum
-// need no shared memory.  fp32 has no tensor-core form of its own accuracy,
-// so FFMA bounds it; per 4 channels a thread reads RPT + 4 vectors for 16 RPT
-// FMAs (as pairs: fma.rn.f32x2).
+// holds a tile of TM query rows; per tile of KT keys S = Q K^T and O += P V
+// from shared memory, each thread RPT rows x KPT keys of S and the same rows x
+// D/16 channels of O, so 16 neighbouring lanes own a row and its maximum and
+// sum need no shared memory.  fp32 has no tensor-core form of its own accuracy,
+// so the FMA pipe bounds it; per 4 channels a thread reads RPT + KPT vectors
+// for 4 RPT KPT FMAs (as pairs: fma.rn.f32x2).
+// 64 rows of 128 channels take 32 keys a tile and not 64, so that two CTAs fit
+// an SM: 2 x 500 tokens over 3001, 8 / 2 heads, 410 us (27 TFLOP/s) against
+// 447; with 8 rows a thread and 4 warps a CTA 567.
+template <int D, int TM>
+constexpr int kSimtKT = D == 128 && TM == 64 ? 32 : 64;
 template <typename T, int D, int TM, bool Q8>
-__global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAttendArgs a) {
-  constexpr int KT = 64, NT = TM == 16 ? 128 : 256, RPT = TM * 16 / NT, CPT = D / 16;
+__global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(PoolAttendArgs a) {
+  constexpr int KT = kSimtKT<D, TM>, KPT = KT / 16, NT = TM == 16 ? 128 : 256, RPT = TM * 16 / NT, CPT = D / 16;
   constexpr int KS = D + 4, PS = KT + 4;
   constexpr int E = 16 / (int)sizeof(T), PPR = D / E;
   static_assert(E == 4, "fp32 rows");
@@ -124,24 +129,24 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
       if constexpr (!Q8) asm volatile("cp.async.wait_group 1;" ::: "memory");
       __syncthreads();
       // S: rows ty * RPT + i, keys tx + 16 j, even and odd channels apart
-      float sc[RPT][4];
+      float sc[RPT][KPT];
       {
-        float2 s2[RPT][4];
+        float2 s2[RPT][KPT];
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+          for (int j = 0; j < KPT; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int e = 0; e < D; e += 4) {
-          float4 kk[4], qq[RPT];
+          float4 kk[KPT], qq[RPT];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * j) * KS + e]);
+          for (int j = 0; j < KPT; ++j) kk[j] = *reinterpret_cast<const float4*>(&Ks[(tx + 16 * j) * KS + e]);
 #pragma unroll
           for (int i = 0; i < RPT; ++i) qq[i] = *reinterpret_cast<const float4*>(&Qs[(ty * RPT + i) * D + e]);
 #pragma unroll
           for (int i = 0; i < RPT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < KPT; ++j) {
               s2[i][j] = ffma2(make_float2(qq[i].x, qq[i].y), make_float2(kk[j].x, kk[j].y), s2[i][j]);
               s2[i][j] = ffma2(make_float2(qq[i].z, qq[i].w), make_float2(kk[j].z, kk[j].w), s2[i][j]);
             }
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[i][j] = s2[i][j].x + s2[i][j].y;
+          for (int j = 0; j < KPT; ++j) sc[i][j] = s2[i][j].x + s2[i][j].y;
       }
       __syncthreads();  // the keys have been read
       if (kt + 1 < kt1) load_tile(kt + 1, 0);
@@ -157,7 +162,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
       for (int i = 0; i < RPT; ++i) {
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KPT; ++j) {
           const int k = tx + 16 * j;
           const int64_t t = (int64_t)kt * KT + k;
           const bool seen = live[(kt & 1) * KT + k] && t <= pos[i] && (a.window <= 0 || t > pos[i] - a.window);
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
         const float f = exp2f(m[i] - ref);
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KPT; ++j) {
           const float p = exp2f(sc[i][j] - ref);
           sum += p;
           Ps[(ty * RPT + i) * PS + tx + 16 * j] = p;
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256) pool_simt_kernel(PoolAtt
 
 template <typename T, int D, int TM, bool Q8>
 cudaError_t launch_simt(const PoolAttendArgs& a, cudaStream_t st) {
-  constexpr int KT = 64;
+  constexpr int KT = kSimtKT<D, TM>;
   constexpr size_t smem = sizeof(float) * (TM * D + KT * (D + 4) + KT * D + TM * (KT + 4)) + 2 * sizeof(int) * KT;
   cudaError_t e = set_smem_once<pool_simt_kernel<T, D, TM, Q8>>(smem);
   if (e == cudaSuccess && a.planned) e = launch_plan<TM, KT>(a, st);
@@ -276,20 +281,17 @@ PoolShape pool_shape(int dtype, int bits, int d, int Hkv, int G, int B, int64_t 
   s.kind = dtype != LOD_DTYPE_BF16 ? 0 : rows > (bits == 8 ? 32 : 64) ? 1 : 2;
   if (s.kind == 2) {
     s.TM = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    s.KT = 128;
     s.ctas = sms;
     s.inline_plan = B <= kInlineSeqs;
   } else if (s.kind == 1) {
     s.TM = 256;
-    s.KT = 128;
     s.ctas = sms;
     s.inline_plan = false;
     const int64_t bytes = capacity * B * Hkv * pool_row_bytes(dtype, bits, d);
     s.max_rounds = (int)(bytes > kRoundBytes * kMaxRounds ? kMaxRounds : (bytes + kRoundBytes - 1) / kRoundBytes);
   } else {
     s.TM = max_new * G <= 16 ? 16 : 64;
-    s.KT = 64;
-    s.ctas = s.TM == 64 && d == 128 ? sms : sms * 2;  // (CTAs an SM holds: 117 KB of shared memory, or 78 and less)
+    s.ctas = sms * 2;  // (two CTAs an SM)
     s.inline_plan = max_new * G <= s.TM && B <= kInlineSeqs;
   }
   const int64_t tiles = N * G / s.TM + B;
