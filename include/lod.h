@@ -436,7 +436,8 @@ typedef struct lod_pool {
  * outside 0 <= new_begin[b] <= new_begin[b + 1] <= N, more than max_new new
  * tokens, fewer tokens than new tokens, or more than max_blocks * block
  * tokens is refused (LOD_ST_BAD_SEQLEN); a table entry outside [0, blocks) is
- * never followed (LOD_ST_BAD_PAGE).  Entries behind a sequence's last block
+ * never followed (LOD_ST_BAD_PAGE, also where only its tile of 128 tokens is
+ * read and a window hides its keys).  Entries behind a sequence's last block
  * are not read.  Sequences without new tokens are fine, and so are rows of
  * the N that no sequence owns: they are left as they were.  Two new tokens
  * must not share a place in the pool.
