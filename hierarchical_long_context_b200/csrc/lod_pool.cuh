@@ -103,7 +103,8 @@ struct PoolAttendArgs {
   // ctas, ... of ctas * rounds.  The CTAs of a round then read about
   // kRoundBytes of the cache between them, which stays in L2 while the
   // row tiles of a head sweep over it at offsets of their own (a 2048-token
-  // chunk over 128K read 15.8 GB from DRAM in one round, for 0.54 GB of cache).
+  // chunk over 128K read 15.8 GB from DRAM in one round, for 0.54 GB of cache;
+  // rounds of 64 MB take 4.21 ms, of 96 MB 4.49, of 40 MB 4.41).
   int max_rounds;
   int32_t* rounds;         // (null: one round)
   int row_bytes;           // stored bytes of a key and its value

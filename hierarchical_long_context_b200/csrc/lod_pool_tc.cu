@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
             for (int e = 0; e < 16; ++e) {
               float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
               // the exponentials are shared out: the special-function unit
-              // takes 8 cycles for a warp's 32, the FMA pipe 7
+              // takes 8 cycles for a warp's 32, the FMA pipe 7 (3 of 8 on the
+              // FMA pipe 4.21 ms for 2048 tokens over 128K, 2 of 8 4.20, 4 of 8 4.33)
               if (e % 8 == 1 || e % 8 == 3 || e % 8 == 6) {
                 t = exp2_fma2(t);
               } else {
