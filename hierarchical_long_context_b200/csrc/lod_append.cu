@@ -24,9 +24,19 @@ __device__ __forceinline__ float2 turn(int64_t pos, float f) {
   return make_float2(c, s);
 }
 
-// Sequence that owns packed row n: the largest b with begin[b] <= n, found by
-// the warp 32 probes at a time; -1 when begin[b + 1] <= n or none starts
-// at or below n.
+// No entry of new_begin before begin[b] lies above it (by a warp).
+__device__ __forceinline__ bool rises(const BatchView& bt, int b) {
+  const int64_t r0 = bt.begin[b];
+  bool above = false;
+#pragma unroll 4
+  for (int i = threadIdx.x & 31; i < b; i += 32) above |= bt.begin[i] > r0;
+  return !__any_sync(0xffffffffu, above);
+}
+
+// Sequence that owns packed row n, -1: none.  It begins at or below n, at or
+// above every earlier entry, and is the first that ends behind n.  Found by the warp
+// 32 probes at a time as the largest b with begin[b] <= n, which is that one
+// while new_begin rises; else by looking at all.
 __device__ __forceinline__ int owner(const BatchView& bt, int64_t n) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = bt.B;  // the answer is in [lo, hi)
@@ -34,12 +44,20 @@ __device__ __forceinline__ int owner(const BatchView& bt, int64_t n) {
     const int step = (hi - lo + 31) / 32;
     const int p = lo + lane * step;
     const unsigned m = __ballot_sync(0xffffffffu, p < hi && bt.begin[p] <= n);
-    if (m == 0) return -1;
+    if (m == 0) return -1;  // (n < begin[0])
     const int top = 31 - __clz(m);
     lo += top * step;
     hi = min(hi, lo + step);
   }
-  return bt.begin[lo] <= n && n < bt.begin[lo + 1] ? lo : -1;
+  if (bt.begin[lo] <= n && n < bt.begin[lo + 1] && rises(bt, lo)) return lo;
+#pragma unroll 1
+  for (int b0 = 0; b0 < bt.B; b0 += 32) {
+    const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < bt.B && bt.begin[b0 + lane + 1] > n);
+    if (m == 0) continue;
+    const int b = b0 + __ffs(m) - 1;
+    return bt.begin[b] <= n && rises(bt, b) ? b : -1;
+  }
+  return -1;
 }
 
 enum Sink { kDense = 0, kPoolRaw = 1, kPoolE4m3 = 2 };

@@ -112,10 +112,14 @@ struct PoolAttendArgs {
 constexpr int64_t kRoundBytes = (int64_t)64 << 20;
 constexpr int kMaxRounds = 8;
 
-// Sequence b of a batch, checked: r0 = first packed row, n = new tokens (0
-// when the sequence is refused), len = tokens.
+// Sequence b of a batch, checked by itself: [r0, r1) = its packed rows, n = new
+// tokens (0 when the sequence is refused), len = tokens.  A sequence that
+// begins below an earlier entry of new_begin is refused too, which only those
+// who look at the whole batch can tell (the work list, the append's owner).
+// Those left have r0 at or above every earlier sequence's r1, so they share no
+// row, and their row tiles number at most N * G / TM + B.
 struct SeqView {
-  int64_t r0, len;
+  int64_t r0, r1, len;
   int n;
   bool ok;
 };
@@ -124,6 +128,7 @@ __device__ __forceinline__ SeqView seq_view(const BatchView& bt, int shift, int 
   const int64_t r0 = bt.begin[b], r1 = bt.begin[b + 1];
   s.len = bt.seq_lens[b];
   s.r0 = r0;
+  s.r1 = r1;
   s.ok = r0 >= 0 && r1 >= r0 && r1 <= bt.N && r1 - r0 <= bt.max_new && s.len >= r1 - r0 &&
          s.len <= ((int64_t)bt.max_blocks << shift);
   s.n = s.ok ? (int)(r1 - r0) : 0;
@@ -204,13 +209,14 @@ __device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t t
 template <int TM, int KT>
 struct Walk {
   const PoolAttendArgs& a;
+  const int64_t* Wb;
   int64_t w0, w, w1, uend;
   Unit u;
   SeqView s;
   int64_t pe;       // end of the piece
   int nt, kt0, kt1, nrow;
 
-  __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* Wb, int part) : a(args) {
+  __device__ __forceinline__ Walk(const PoolAttendArgs& args, const int64_t* wb, int part) : a(args), Wb(wb) {
     const int64_t total = Wb[a.batch.B], share = list_share(a, total);
     w0 = w = part * share;
     w1 = w0 + share < total ? w0 + share : total;
@@ -242,9 +248,9 @@ struct Walk {
         u.i = 0;
         if (++u.h == a.pool.Hkv) {
           u.h = 0;
-          do {
-            s = seq_view(a.batch, a.pool.shift, ++u.b);
-          } while (s.n == 0);
+          do ++u.b;
+          while (Wb[u.b + 1] == Wb[u.b]);  // (no new tokens, or refused)
+          s = seq_view(a.batch, a.pool.shift, u.b);
           nt = (s.n * a.G + TM - 1) / TM;
         }
       }
@@ -253,7 +259,7 @@ struct Walk {
     } while (kt0 == kt1);
   }
   // (after the walk; by one thread)
-  __device__ __forceinline__ void record(const int64_t* Wb, int part) const {
+  __device__ __forceinline__ void record(int part) const {
     MergeRec r = {0, 0, 0, 0, 0};
     if (w0 < w1 && uend > w1 && u.first() >= w0 && u.first() < w1) {
       const int64_t share = list_share(a, Wb[a.batch.B]);
@@ -270,22 +276,38 @@ struct Walk {
 constexpr int kInlineSeqs = 256;
 
 // Wb of sequences with one row tile each, by the whole CTA (at least one
-// warp); ends with a CTA barrier.
+// warp); ends with a CTA barrier.  While new_begin rises no entry lies above a
+// later one; the running maximum is taken only once it has fallen.
 template <int TM, int KT>
 __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb) {
   if (threadIdx.x < 32) {
-    int64_t at = 0;
+    int64_t at = 0, top = INT64_MIN;
+    bool fell = false;
     if (threadIdx.x == 0) Wb[0] = 0;
     for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
       const int b = b0 + threadIdx.x;
-      int64_t n = 0;
+      int64_t n = 0, r0 = INT64_MIN;
+      bool falls = false;
       if (b < a.batch.B) {
         const SeqView s = seq_view(a.batch, a.pool.shift, b);
+        r0 = s.r0;
+        falls = s.r1 < s.r0;
         if (s.n > 0) {
           int lo, hi;
           row_tile_keys<TM, KT>(s, a.G, a.window, 0, lo, hi);
           n = (int64_t)(hi - lo + kUnitCost) * a.pool.Hkv;
         }
+      }
+      fell |= __any_sync(0xffffffffu, falls) != 0;
+      if (fell) {
+        int64_t m = r0 > top ? r0 : top;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, m, o);
+          if ((int)threadIdx.x >= o && x > m) m = x;
+        }
+        if (r0 < m) n = 0;
+        top = __shfl_sync(0xffffffffu, m, 31);
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -300,22 +322,40 @@ __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb
 }
 
 // Rows of refused sequences: out = 0, lse = -inf.  Every CTA of the grid calls
-// this with all its threads; the CTAs share the sequences out.
+// this with all its threads; the CTAs share the sequences out.  A refused
+// sequence may name rows of another that is not: of its rows it clears those
+// that no earlier sequence reaches.  (The entries of new_begin up to b rise
+// and fall from begin[0] to their maximum, so each row between these two is
+// passed by a rising pair first: its sequence owns the row, or clears it.)
 template <typename T, int D>
-__device__ __forceinline__ void clear_refused(const PoolAttendArgs& a) {
+__device__ __forceinline__ void clear_refused(const PoolAttendArgs& a, const int64_t* Wb) {
   constexpr int N16 = D * (int)sizeof(T) / 16;
   for (int b = blockIdx.x; b < a.batch.B; b += gridDim.x) {
+    if (Wb[b + 1] > Wb[b]) continue;
     const SeqView s = seq_view(a.batch, a.pool.shift, b);
-    if (s.ok) continue;
+    if (s.ok && s.n == 0) continue;
     if (threadIdx.x == 0) set_status(a.status, LOD_ST_BAD_SEQLEN);
-    int64_t r0 = a.batch.begin[b], r1 = a.batch.begin[b + 1];
-    if (r0 < 0) r0 = 0;
-    if (r1 > a.batch.N) r1 = a.batch.N;
-    for (int64_t x = threadIdx.x; r0 < r1 && x < (r1 - r0) * a.Hq * N16; x += blockDim.x) {
-      const int64_t row = x / N16, t = r0 + row / a.Hq, h = row % a.Hq;
-      const int c = (int)(x % N16);
-      reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.ot + h * a.oh)[c] = make_uint4(0, 0, 0, 0);
-      if (c == 0 && a.lse) a.lse[t * a.Hq + h] = -INFINITY;
+    int64_t top = s.r0;
+    for (int i = threadIdx.x & 31; i < b; i += 32)
+      if (a.batch.begin[i] > top) top = a.batch.begin[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int64_t x = __shfl_xor_sync(0xffffffffu, top, o);
+      if (x > top) top = x;
+    }
+    const int64_t end = s.r1 < a.batch.N ? s.r1 : a.batch.N, begin0 = a.batch.begin[0];
+#pragma unroll 1
+    for (int below = 0; below < 2; ++below) {  // its rows above every earlier entry, and those below the first one
+      int64_t r0 = below ? s.r0 : top;
+      const int64_t r1 = below && begin0 < end ? begin0 : end;
+      if (below && s.r0 >= begin0) break;
+      if (r0 < 0) r0 = 0;
+      for (int64_t x = threadIdx.x; r0 < r1 && x < (r1 - r0) * a.Hq * N16; x += blockDim.x) {
+        const int64_t row = x / N16, t = r0 + row / a.Hq, h = row % a.Hq;
+        const int c = (int)(x % N16);
+        reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.ot + h * a.oh)[c] = make_uint4(0, 0, 0, 0);
+        if (c == 0 && a.lse) a.lse[t * a.Hq + h] = -INFINITY;
+      }
     }
   }
 }

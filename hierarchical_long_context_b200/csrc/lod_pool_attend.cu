@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(Pool
     plan_inline<TM, KT>(a, wb_s);
     Wb = wb_s;
   }
-  clear_refused<T, D>(a);
+  clear_refused<T, D>(a, Wb);
   Walk<TM, KT> w(a, Wb, blockIdx.x);
   for (; w.more(); w.next()) {
     const Unit& u = w.u;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(Pool
       }
     }
   }
-  if (tid == 0) w.record(Wb, blockIdx.x);
+  if (tid == 0) w.record(blockIdx.x);
 }
 
 template <typename T, int D, int TM, bool Q8>

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     plan_inline<RQ, kKT>(a, wb_s);
     Wb = wb_s;
   }
-  clear_refused<__nv_bfloat16, D>(a);
+  clear_refused<__nv_bfloat16, D>(a, Wb);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           if (j == T - 1) mma_commit_if(lead, &q_empty[k & 1]);
         }
       }
-      if (lane == 0) w.record(Wb, blockIdx.x);
+      if (lane == 0) w.record(blockIdx.x);
       if (c > 0) {
         mma_commit_if(lead, &fin[0]);
         (void)mbar_wait(&fin[0], 0, a.status);

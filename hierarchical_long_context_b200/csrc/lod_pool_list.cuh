@@ -9,14 +9,16 @@ namespace {
 
 // ---------------------------------------------------------------- work list
 
-// Inclusive scan of one value per thread over the CTA (1024 threads);
-// `total` receives the sum.
+// Inclusive scan of one value per thread over the CTA (1024 threads), of sums
+// or of maxima; `total` receives that of all.
+template <bool kMax>
 __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  auto join = [](int64_t x, int64_t y) { return !kMax ? x + y : x > y ? x : y; };
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
+    if (lane >= o) v = join(v, x);
   }
   if (lane == 31) warp_sums[w] = v;
   __syncthreads();
@@ -25,12 +27,12 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
+      if (lane >= o) s = join(s, x);
     }
     warp_sums[lane] = s;
   }
   __syncthreads();
-  if (w > 0) v += warp_sums[w - 1];
+  if (w > 0) v = join(v, warp_sums[w - 1]);
   *total = warp_sums[31];
   __syncthreads();
   return v;
@@ -43,12 +45,24 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
   pdl_launch_dependents();
   __shared__ int64_t ws[32];
   const int B = a.batch.B, lane = threadIdx.x & 31;
-  int64_t at = 0, total;
+  int64_t at = 0, total, top = INT64_MIN;
+  bool fell = false;  // (as in plan_inline)
   for (int b0 = 0; b0 < B; b0 += 1024) {
     const int b = b0 + threadIdx.x;
-    int64_t n = 0;
-    if (b < B) n = ((int64_t)seq_view(a.batch, a.pool.shift, b).n * a.G + TM - 1) / TM;
-    const int64_t s = block_scan(n, ws, &total);
+    int64_t n = 0, r0 = INT64_MIN;
+    bool falls = false;
+    if (b < B) {
+      const SeqView q = seq_view(a.batch, a.pool.shift, b);
+      n = ((int64_t)q.n * a.G + TM - 1) / TM;
+      r0 = q.r0;
+      falls = q.r1 < q.r0;
+    }
+    fell |= __syncthreads_or(falls) != 0;
+    if (fell) {
+      if (r0 < block_scan<true>(r0 > top ? r0 : top, ws, &total)) n = 0;
+      top = total;
+    }
+    const int64_t s = block_scan<false>(n, ws, &total);
     if (b < B) a.RT[b + 1] = (int32_t)(at + s);
     at += total;
   }
@@ -82,7 +96,7 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
   at = 0;
   for (int b0 = 0; b0 < B; b0 += 1024) {
     const int b = b0 + threadIdx.x;
-    const int64_t s = block_scan(b < B ? a.Wb[b + 1] : 0, ws, &total);
+    const int64_t s = block_scan<false>(b < B ? a.Wb[b + 1] : 0, ws, &total);
     if (b < B) a.Wb[b + 1] = at + s;
     at += total;
   }
@@ -92,11 +106,11 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
     for (int b0 = 0; b0 < B; b0 += 1024) {
       const int b = b0 + threadIdx.x;
       int64_t n = 0;
-      if (b < B) {
+      if (b < B && a.RT[b + 1] > a.RT[b]) {
         const SeqView s = seq_view(a.batch, a.pool.shift, b);
-        if (s.n > 0) n = a.window > 0 && s.len > a.window + s.n ? a.window + s.n : s.len;
+        n = a.window > 0 && s.len > a.window + s.n ? a.window + s.n : s.len;
       }
-      block_scan(n, ws, &total);
+      block_scan<false>(n, ws, &total);
       keys += total;
     }
     if (threadIdx.x == 0) {

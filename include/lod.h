@@ -433,9 +433,10 @@ typedef struct lod_pool {
  * the last of its seq_lens[b] tokens; token t of a sequence lives in block
  * block_table[b][t / block] at row t % block.
  * The device values are checked by the kernels: a sequence with new_begin
- * outside 0 <= new_begin[b] <= new_begin[b + 1] <= N, more than max_new new
- * tokens, fewer tokens than new tokens, or more than max_blocks * block
- * tokens is refused (LOD_ST_BAD_SEQLEN); a table entry outside [0, blocks) is
+ * outside 0 <= new_begin[b] <= new_begin[b + 1] <= N, one whose new_begin[b]
+ * lies below an earlier entry, one with more than max_new new tokens, fewer
+ * tokens than new tokens, or more than max_blocks * block tokens is refused
+ * (LOD_ST_BAD_SEQLEN), so no row has two owners; a table entry outside [0, blocks) is
  * never followed (LOD_ST_BAD_PAGE, also where only its tile of 128 tokens is
  * read and a window hides its keys).  Entries behind a sequence's last block
  * are not read.  Sequences without new tokens are fine, and so are rows of
@@ -509,7 +510,8 @@ int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, s
  * row is taken relative to the largest row of its 128 tokens and loses
  * precision when it is smaller than 2^-14 of it.
  * Keys in a bad block are left out; a row that sees no key then, and every
- * row of a refused sequence that lies in [0, N), gets out = 0 and lse = -inf.
+ * row of a refused sequence that lies in [0, N) and belongs to no other, gets
+ * out = 0 and lse = -inf.
  */
 int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void* q, const int64_t q_strides[2],
                         void* out, const int64_t out_strides[2], float* lse, int64_t window, float scale, void* ws,

@@ -1,0 +1,138 @@
+"""Batches of the block pool whose new_begin falls, and batches of many sequences, on the GPU: which sequences a call
+takes, that no row is given to two, that the workspace is not left, and the values against the 64-bit forms."""
+import math
+
+import pytest
+import torch
+
+import hierarchical_long_context_b200 as lod
+from hierarchical_long_context_b200 import api
+from tests import pooltest as pt
+from tests.test_gpu_pool import BF, F32, ST, close, gen, make_pool, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def taken(begin, lens, N, max_new):
+    """The sequences of a batch that are not refused, and the rows of [0, N) that only refused ones name."""
+    ok, top = [], -math.inf
+    for b, L in enumerate(lens):
+        r0, r1 = begin[b], begin[b + 1]
+        top = max(top, r0)
+        ok.append(0 <= r0 <= r1 <= N and r1 - r0 <= min(max_new, L) and (r0 == top or r0 == r1))
+    owned, named = set(), set()
+    for b in range(len(lens)):
+        rows = range(max(begin[b], 0), min(begin[b + 1], N))
+        if ok[b]:
+            assert owned.isdisjoint(rows)
+            owned.update(rows)
+        else:
+            named.update(rows)
+    return ok, sorted(owned), sorted(named - owned)
+
+
+def walk(begin, lens, N, max_new, Hq, Hkv, d, block, dtype, bits, seed):
+    """Append and attention of one batch, checked row by row."""
+    B = len(lens)
+    ok, owned, cleared = taken(begin, lens, N, max_new)
+    g = gen(seed)
+    pool, table = make_pool(g, lens, block, Hq, Hkv, d, dtype, bits)
+    batch = api.PoolBatch(table, torch.tensor(lens, device="cuda"), torch.tensor(begin, device="cuda"), tokens=N,
+                          max_new=max_new)
+    q, k, v = randn(g, N, Hq, d, dtype=dtype), randn(g, N, Hkv, d, dtype=dtype), randn(g, N, Hkv, d, dtype=dtype)
+
+    # the append writes the new rows of the sequences that are taken, and nothing else
+    want = [None if x is None else x.clone() for x in (pool.K, pool.V, pool.Ke, pool.Ve)]
+    for b in range(B):
+        if ok[b] and begin[b + 1] > begin[b]:
+            n = begin[b + 1] - begin[b]
+            t = torch.arange(lens[b] - n, lens[b], device="cuda")
+            blk, off = table[b].long()[t // block], t % block
+            for X, E, x in ((want[0], want[2], k), (want[1], want[3], v)):
+                rows = x[begin[b]:begin[b + 1]]
+                if bits:
+                    X[blk, :, off], E[blk, :, off] = pt.quantise64(rows)
+                else:
+                    X[blk, :, off] = rows
+    rope = api.Rope()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((N, Hq, d), 9.0, dtype=dtype, device="cuda")
+    lod.lod_pool_append(pool, batch, k, v, rope=rope, q=q, q_out=out, status=status)
+    assert int(status) == (0 if all(ok) else ST["seqlen"])
+    mine = torch.zeros(N, dtype=torch.bool, device="cuda")
+    mine[owned] = True
+    assert torch.equal(out[mine], q[mine]) and (out[~mine] == 9).all()
+    for X, Y in zip((pool.K, pool.V, pool.Ke, pool.Ve), want):
+        assert X is None or torch.equal(X.view(torch.uint8), Y.view(torch.uint8))
+
+    # the attention, with a workspace of the size that was asked for and a guard behind it
+    need = api.pool_workspace_bytes(pool, batch)
+    buf = torch.zeros(need + (1 << 20), dtype=torch.uint8, device="cuda")
+    buf[need:] = 0x5a
+    out.fill_(9.0)
+    lse = torch.full((N, Hq), 9.0, device="cuda")
+    lod.lod_pool_attend(pool, batch, q, out=out, lse=lse, ws=buf[:need])
+    assert lod.lod_get_status(buf[:need]) == (0 if all(ok) else ST["seqlen"])
+    assert (buf[need:] == 0x5a).all()
+    gone = torch.zeros(N, dtype=torch.bool, device="cuda")
+    gone[cleared] = True
+    assert (out[gone] == 0).all() and (lse[gone] == -math.inf).all()
+    assert (out[~gone & ~mine] == 9).all() and (lse[~gone & ~mine] == 9).all()
+    for b in range(0, B, 1 if B < 100 else 7):
+        r0, r1 = begin[b], begin[b + 1]
+        if ok[b] and r1 > r0:
+            o, z, to, tz = pt.attend64(pool, table[b:b + 1], lens[b:b + 1], [0, r1 - r0], q[r0:r1])
+            close(out[r0:r1], o, to, "out %d" % b)
+            close(lse[r0:r1], z, tz, "lse %d" % b)
+
+
+FALLING = [
+    ([0, 6, 0, 6], 6),                     # two sequences of the same rows
+    ([0, 5, 2, 8, 11], 6),                 # rows 5 .. 7 are named by a refused sequence alone
+    ([6, 9, 1, 4, 9, 12], 5),              # rows below the first entry
+    ([0, 40, 5, 8, 8, 45, 50], 6),         # a refused one that reaches over others
+    ([2, 4, 4, 3, 3, 9, 9], 6),            # empty ones in the fall
+    ([0, 3, 1 << 40, 3, 6], 6),
+    ([-3, 2, 5, 4, 9], 6),
+]
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 0)])
+@pytest.mark.parametrize("begin, max_new", FALLING)
+def test_new_begin_that_falls(begin, max_new, dtype, bits):
+    lens = [70 + 13 * b for b in range(len(begin) - 1)]
+    walk(begin, lens, 51, max_new, 4, 2, 64, 16, dtype, bits, 101)
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 8)])
+@pytest.mark.parametrize("n", [40, 700])
+def test_long_sequences_of_the_same_rows(n, dtype, bits):
+    """The list holds the row tiles of N rows: a second and third sequence of the same ones would not fit."""
+    walk([0, n, 0, n, 0, n, n + 20], [n + 30, n + 5, n + 60, n + 9, n, 90], n + 25, n, 8, 1, 128, 32, dtype, bits, 102)
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (F32, 0)])
+@pytest.mark.parametrize("G, B", [(1, 33), (2, 70), (8, 300), (1, 1100), (16, 1060)])
+@pytest.mark.parametrize("falls", [False, True])
+def test_batches_of_many_sequences(falls, G, B, dtype, bits):
+    """More sequences than a warp's probes, than a CTA lays out by itself (256), than a pass of the plan (1024); with
+    G = 16 a sequence of 3 new tokens makes 48 rows."""
+    g = torch.Generator().manual_seed(B)
+    new = torch.randint(0, 4, (B,), generator=g).tolist()
+    lens = [n + int(x) for n, x in zip(new, torch.randint(0, 60, (B,), generator=g))]
+    lens = [max(L, 1) for L in lens]
+    begin = [1]
+    for n in new:
+        begin.append(begin[-1] + n)
+    N = begin[-1] + 3
+    if falls:  # everything from one entry on begins again lower down
+        at = B - B // 4
+        down = begin[at] // 2
+        begin = begin[:at] + [x - down for x in begin[at:]]
+    walk(begin, lens, N, 3, G, 1, 64, 16, dtype, bits, 103)
