@@ -454,40 +454,44 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           l += (l2.x + l2.y) * (Q8 ? exp2i(-df - (int)kUp) : 1.f);
         }
       }
-      if (!go) break;
       // ---- the rows' results
-      go = __all_sync(0xffffffffu, wait(&o_full[s], no++ & 1u));
-      if (!go) break;
-      tc::fence_after_sync();
-      const bool whole = w.whole();
-      const float unit = Q8 ? exp2i(cv - 127 - (int)kUp) : 1.f;
-      const float inv = l > 0.f || l != l ? unit / l : 0.f;
-      const int64_t at = (int64_t)w.slot(part) * kTM + s * 128 + r;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh;
+      if (go) go = __all_sync(0xffffffffu, wait(&o_full[s], no++ & 1u));
+      if (go) {
+        tc::fence_after_sync();
+        const bool whole = w.whole();
+        const float unit = Q8 ? exp2i(cv - 127 - (int)kUp) : 1.f;
+        const float inv = l > 0.f || l != l ? unit / l : 0.f;
+        const int64_t at = (int64_t)w.slot(part) * kTM + s * 128 + r;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (w.s.r0 + tok) * a.ot + (int64_t)head * a.oh;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        float o[32];
-        tc::tmem_ld32(to + 32 * q, o);
-        if (mine && whole) {
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          tc::tmem_ld32(to + 32 * q, o);
+          if (mine && whole) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4*>(out)[4 * q + e] =
-                make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                           pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                           pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-        } else if (mine) {
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(out)[4 * q + e] =
+                  make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                             pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                             pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          } else if (mine) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<float4*>(a.part + at * D)[8 * q + e] =
-                make_float4(o[4 * e] * unit, o[4 * e + 1] * unit, o[4 * e + 2] * unit, o[4 * e + 3] * unit);
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(a.part + at * D)[8 * q + e] =
+                  make_float4(o[4 * e] * unit, o[4 * e + 1] * unit, o[4 * e + 2] * unit, o[4 * e + 3] * unit);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (mine) {
+          if (!whole) a.ml[at] = make_float2(m, l);
+          else if (a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
+        }
+        tc::fence_before_sync();  // O_s is read before the next unit's weights are announced
       }
-      if (mine) {
-        if (!whole) a.ml[at] = make_float2(m, l);
-        else if (a.lse) a.lse[(w.s.r0 + tok) * a.Hq + head] = (m + log2f(l)) * 0.6931471805599453f;
-      }
-      tc::fence_before_sync();  // O_s is read before the next unit's weights are announced
+      __syncwarp();
+      // a wait that gave up is one warp's own: the four leave together, as the
+      // next unit opens with a barrier of theirs, which has no limit
+      go = !bar_red_or(1 + s, 128, !go);
     }
   } else if constexpr (Q8) {
     // ============================================================== codes to bf16 tiles
