@@ -397,7 +397,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           }
           float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], y[60]);
           top = max3(max3(top, y[61], y[62]), y[63], y[63]) * scl;
-          if (top != top) l = NAN;  // a NaN score: the row's results are NaN, whatever its weights become
+          // a NaN score, or an infinite one (inf - inf): the row's results are
+          // NaN, whatever its weights become
+          if (!(top < INFINITY)) l = NAN;
           const bool start = j == 0 && u == 0;
           const bool need = top > m + kTau || start;
           if (__any_sync(0xffffffffu, need || (fv != 1.f && u == 0))) {

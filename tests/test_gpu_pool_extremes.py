@@ -1,0 +1,87 @@
+"""Attention over the block pool at the edges of its number formats, on the GPU: infinite scores, scales that
+underflow, value rows of zeros and of very different sizes, NaN in rows that a query does not see."""
+import math
+
+import pytest
+import torch
+
+import hierarchical_long_context_b200 as lod
+from hierarchical_long_context_b200 import api
+from tests import pooltest as pt
+from tests.test_gpu_pool import BF, F32, close, gen, make_batch, randn
+
+pytestmark = pytest.mark.gpu
+LN2 = math.log(2.0)
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def pool_of(rows, block, Hq, dtype, bits, g):
+    """A pool that holds the sequences' rows [(k, v)], each [length, Hkv, d], its blocks dealt out at random."""
+    Hkv, d = rows[0][0].shape[1:]
+    need = [-(-len(k) // block) for k, _ in rows]
+    order = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(rows), max(need)), -1, dtype=torch.int32, device="cuda")
+    pool = api.Pool.empty(sum(need), block, Hq, Hkv, d, dtype, bits)
+    at = 0
+    for b, (k, v) in enumerate(rows):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        t = torch.arange(len(k), device="cuda")
+        blk, off = table[b].long()[t // block], t % block
+        for X, E, x in ((pool.K, pool.Ke, k), (pool.V, pool.Ve, v)):
+            if bits:
+                X[blk, :, off], E[blk, :, off] = pt.quantise64(x.to(dtype))
+            else:
+                X[blk, :, off] = x.to(dtype)
+    return pool, table
+
+
+def attend(pool, table, lens, new, q, window=0, scale=0.0):
+    begin, batch = make_batch(table, lens, new)
+    out = torch.full_like(q, 9.0)
+    lse = torch.full(q.shape[:2], 9.0, device="cuda")
+    ws = api.pool_workspace(pool, batch)
+    lod.lod_pool_attend(pool, batch, q, out=out, lse=lse, window=window, scale=scale, ws=ws)
+    return begin, out, lse, lod.lod_get_status(ws)
+
+
+def check(pool, table, lens, new, q, scale=0.0):
+    begin, out, lse, status = attend(pool, table, lens, new, q, scale=scale)
+    assert status == 0
+    o, z, to, tz = pt.attend64(pool, table, lens, begin, q, 0, scale)
+    close(lse, z, tz, "lse")
+    close(out, o, to, "out")
+
+
+# ------------------------------------------------------------------ infinite scores
+
+@pytest.mark.parametrize("dtype, d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("n", [1, 60, 150])
+def test_a_key_of_infinite_score_makes_the_row_nan(n, dtype, d):
+    """An infinite key channel at each place of a tile's first 32 keys: a query on its positive side has the weight
+    inf - inf; on its negative side the key has none."""
+    B, L, Hq, Hkv = 32, 128 + n + 9, 4, 2
+    g = gen(201)
+    rows = [(randn(g, L, Hkv, d), randn(g, L, Hkv, d)) for _ in range(B)]
+    at = [b if n == 1 or b % 2 else L - n + b // 2 for b in range(B)]  # among the old keys, or the new ones
+    for b in range(B):
+        rows[b][0][at[b], :, 3] = math.inf
+    pool, table = pool_of(rows, 32, Hq, dtype, 0, g)
+    q = randn(g, B * n, Hq, d, dtype=dtype)
+    begin, out, lse, status = attend(pool, table, [L] * B, [n] * B, q)
+    assert status == 0
+    bad = [torch.arange(L, device="cuda") == at[b] for b in range(B)]
+    o, z, to, tz = pt.attend64(pool, table, [L] * B, begin, q, bad_keys=bad)
+    pos = (torch.arange(n, device="cuda") + L - n).repeat(B)
+    sees = pos >= torch.tensor(at, device="cuda").repeat_interleave(n)
+    hit = sees[:, None] & (q[..., 3] > 0)
+    assert 0.2 < hit.float().mean() < 0.6
+    assert torch.isnan(out[hit]).all(), "%d of %d" % (int((~torch.isnan(out[hit])).any(-1).sum()), int(hit.sum()))
+    assert torch.isnan(lse[hit]).all()
+    close(out[~hit], o[~hit], to[~hit], "out")
+    close(lse[~hit], z[~hit], tz[~hit], "lse")
