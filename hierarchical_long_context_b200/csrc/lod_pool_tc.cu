@@ -1,5 +1,7 @@
 // lod_pool_tc.cu -- exact attention of many new tokens over the block pool on the
 // tensor cores (tcgen05, TMEM accumulators, TMA): 256 query rows per unit.
+#include <cfloat>
+
 #include "lod_pool_list.cuh"
 #include "lod_pool_tc.cuh"
 
@@ -296,14 +298,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const int tok = g / G, head = w.u.h * G + g % G;
       const int p0 = (int)(w.s.len - w.s.n);
       const int pos = p0 + tok;
-      float row_scale = a.scale_log2;
+      int eq = 0;  // (8-bit) the query row's power of two
       {
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + (w.s.r0 + tok) * a.qt + (int64_t)head * a.qh;
         uint4 x[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) x[i] = mine ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-        if (Q8) row_scale = a.scale_log2 * exp2i(query_f16<D>(x));
+        if (Q8) eq = query_f16<D>(x);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(Qs + (i >> 3) * kHalfBytes + sw_off(r, i)) = x[i];
         tc::fence_proxy_async();
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       int cv = 0;  // (8-bit) O_s is in units of 2^(cv - 127 - kUp)
       for (int j = 0; j < T && go; ++j, c += 2) {
         const int kt = w.kt0 + j;
-        float scl = row_scale;
+        float scl = a.scale_log2;
         int df = 0;      // (8-bit) this tile's value exponent above cv
         float fv = 1.f;  // and the factor O_s takes for a new cv
         const bool ragged = kt * kKT + 127 >= w.s.len || kt * kKT < first_unit || unit_bad;  // V rows that are no keys
@@ -344,7 +346,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         }
         if constexpr (Q8) {
           const int ck = info_s[(c >> 1) & 15], e = max(info_s[16 + ((c >> 1) & 15)], 7);
-          scl *= exp2i(max(ck, 7) - 127);
+          // the powers of two are joined first, and the factor stays in fp32's
+          // normal range: 0 or infinity times a masked or zero score is NaN
+          // (scores off by that are below 2^-90)
+          scl *= exp2i(min(max(eq + max(ck, 7) - 127, -126), 127));
+          scl = fminf(fmaxf(scl, FLT_MIN), FLT_MAX);
           if (j == 0) cv = e;
           if (e > cv + 1) {
             fv = exp2i(max(cv - e, -126));

@@ -85,3 +85,28 @@ def test_a_key_of_infinite_score_makes_the_row_nan(n, dtype, d):
     assert torch.isnan(lse[hit]).all()
     close(out[~hit], o[~hit], to[~hit], "out")
     close(lse[~hit], z[~hit], tz[~hit], "lse")
+
+
+# ------------------------------------------------------------------ scales below fp32's range
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 60, 300])
+@pytest.mark.parametrize("qmul, scale", [(2.0 ** -15, 0.0), (2.0 ** -60, 0.0), (1.0, 1e-30), (2.0 ** -100, 1e-20)])
+def test_key_tiles_of_zeros_and_bad_blocks_with_small_queries(qmul, scale, n, dtype, bits):
+    """A tile of zero keys has the smallest exponent a row can have; with a small query the product of the scale and
+    both powers of two lies below fp32's range."""
+    g = gen(202)
+    L, Hq, Hkv, d = 520, 4, 2, 64
+    k, v = randn(g, L, Hkv, d), randn(g, L, Hkv, d)
+    k[128:384] = 0
+    pool, table = pool_of([(k, v)], 64, Hq, dtype, bits, g)
+    check(pool, table, [L], [n], (randn(g, n, Hq, d) * qmul).to(dtype), scale)
+    gone = torch.zeros(L, dtype=torch.bool, device="cuda")
+    gone[128:256] = True
+    safe = table.clone()
+    table[0, 2:4] = -1
+    q = (randn(g, n, Hq, d) * qmul).to(dtype)
+    begin, out, lse, _ = attend(pool, table, [L], [n], q, scale=scale)
+    o, z, to, tz = pt.attend64(pool, safe, [L], begin, q, 0, scale, bad_keys=[gone])
+    close(lse, z, tz, "lse")
+    close(out, o, to, "out")
