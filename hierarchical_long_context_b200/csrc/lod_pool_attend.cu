@@ -50,7 +50,9 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(Pool
     const int kt0 = w.kt0, kt1 = w.kt1, nrow = w.nrow;
     const int64_t row0 = u.i * TM;
     const int32_t* table = a.batch.table + (int64_t)u.b * a.batch.max_blocks;
-    const int64_t first_unit = a.window > 0 ? s.len - s.n + row0 / a.G - a.window + 1 : 0;  // (earlier keys: no row's)
+    // (earlier and later keys are no row's)
+    const int64_t first_unit = a.window > 0 ? s.len - s.n + row0 / a.G - a.window + 1 : 0;
+    const int64_t last_unit = s.len - s.n + (row0 + nrow - 1) / a.G;
 
     __syncthreads();
     for (int x = tid; x < TM * PPR; x += NT) {
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(Pool
         const int k = x / PPR, c = x % PPR;
         const int64_t t = (int64_t)kt * KT + k;
         int64_t blk = -1;
-        if (t < s.len && t >= first_unit) {
+        if (t <= last_unit && t >= first_unit) {
           blk = table[t >> a.pool.shift];
           if (blk < 0 || blk >= a.pool.blocks) {
             blk = -1;

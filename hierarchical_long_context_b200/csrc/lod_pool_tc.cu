@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const int first = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;  // this row's keys
       const int first_hi = a.window > 0 && pos_hi - a.window + 1 > 0 ? (int)(pos_hi - a.window + 1) : 0;
 
-      // keys of no row of the unit's two tiles
-      const int u0 = p0 + (int)w.u.i * kTM / G;
+      // keys of no row of the unit's two tiles: before first_unit, behind last_unit
+      const int u0 = p0 + (int)w.u.i * kTM / G, last_unit = p0 + ((int)w.u.i * kTM + w.nrow - 1) / G;
       const int first_unit = a.window > 0 && u0 - a.window + 1 > 0 ? (int)(u0 - a.window + 1) : 0;
 
       float m = -INFINITY, l = 0.f;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         float scl = a.scale_log2;
         int df = 0;      // (8-bit) this tile's value exponent above cv
         float fv = 1.f;  // and the factor O_s takes for a new cv
-        const bool ragged = kt * kKT + 127 >= w.s.len || kt * kKT < first_unit || unit_bad;  // V rows that are no keys
+        const bool ragged = kt * kKT + 127 > last_unit || kt * kKT < first_unit || unit_bad;  // V rows that are no keys
         if (Q8 || ragged) {
           // The tile's values (8-bit: with them its exponents).  A barrier's
           // parity tells a phase only from the one before it: the scores are
@@ -359,11 +359,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           df = max(e - cv, -60);
         }
         if (ragged) {
-          // P's zeros must not meet what the pool holds behind the length or
-          // before every row's window, or what shared memory held before:
-          // those V rows become zero
+          // P's zeros must not meet what the pool holds behind every row's
+          // position or before every row's window, or what shared memory held
+          // before: those V rows become zero
           const int t = kt * kKT + r, i = t >> shift;
-          if (t >= w.s.len || t < first_unit || table[i] < 0 || table[i] >= a.pool.blocks) {
+          if (t > last_unit || t < first_unit || table[i] < 0 || table[i] >= a.pool.blocks) {
             unsigned char* v = sm + S::off_KV + (size_t)((c + 1) % NS) * S::kTile;
 #pragma unroll
             for (int q = 0; q < D / 8; ++q)

@@ -110,3 +110,28 @@ def test_key_tiles_of_zeros_and_bad_blocks_with_small_queries(qmul, scale, n, dt
     o, z, to, tz = pt.attend64(pool, safe, [L], begin, q, 0, scale, bad_keys=[gone])
     close(lse, z, tz, "lse")
     close(out, o, to, "out")
+
+
+# ------------------------------------------------------------------ NaN behind a query
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 0), (F32, 8)])
+@pytest.mark.parametrize("G, n, T", [(16, 130, 120), (4, 300, 280), (1, 700, 600), (64, 70, 66)])
+def test_a_nan_value_reaches_no_queries_far_before_it(G, n, T, dtype, bits):
+    """New token T's value row is NaN: queries of its own sequence more than 256 query rows before T's do not see it,
+    also where its key shares a tile with theirs."""
+    g = gen(205)
+    L, Hkv, d = 256 + n, 2, 64
+    k, v = randn(g, L, Hkv, d, dtype=dtype), randn(g, L, Hkv, d, dtype=dtype)
+    pool, table = pool_of([(k, v)], 32, G * Hkv, dtype, bits, g)
+    _, batch = make_batch(table, [L], [n])
+    v[L - n + T, :, 5] = math.nan
+    lod.lod_pool_append(pool, batch, k[L - n:], v[L - n:])
+    q = randn(g, n, G * Hkv, d, dtype=dtype)
+    begin, out, lse, status = attend(pool, table, [L], [n], q)
+    assert status == 0
+    o, z, to, tz = pt.attend64(pool, table, [L], begin, q)
+    close(lse, z, tz, "lse")
+    far = T - -(-256 // G)
+    assert far > 0 and torch.isfinite(o[:far]).all()
+    close(out[:far], o[:far], to[:far], "out")
+    assert torch.isnan(out[T:, :, 5]).all()
