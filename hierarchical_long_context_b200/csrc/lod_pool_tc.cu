@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       const int first_unit = a.window > 0 && u0 - a.window + 1 > 0 ? (int)(u0 - a.window + 1) : 0;
 
       float m = -INFINITY, l = 0.f;
-      int cv = 0;  // (8-bit) O_s is in units of 2^(cv - 127 - kUp)
+      int cv = 0, cm = 0;  // (8-bit) O_s is in units of 2^(cv - 127 - kUp); the largest tile exponent so far
       for (int j = 0; j < T && go; ++j, c += 2) {
         const int kt = w.kt0 + j;
         float scl = a.scale_log2;
@@ -351,10 +351,17 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
           // (scores off by that are below 2^-90)
           scl *= exp2i(min(max(eq + max(ck, 7) - 127, -126), 127));
           scl = fminf(fmaxf(scl, FLT_MIN), FLT_MAX);
-          if (j == 0) cv = e;
-          if (e > cv + 1) {
-            fv = exp2i(max(cv - e, -126));
-            cv = e;
+          // The unit of O_s follows the tiles up, and down where their values
+          // are much smaller: a weight carries 2^(e - cv), and f16 drops what
+          // lies 2^-30 below the largest.  It stays within 2^60 of the
+          // largest, so that O_s (at most 2^44 of its unit) stays in fp32;
+          // tiles of zeros leave it where it is.
+          if (j == 0) cv = cm = e;
+          cm = max(cm, e);
+          if (e > cv + 1 || (e < cv - 8 && e > 7)) {
+            const int to = max(e, cm - 60);
+            fv = exp2i(max(cv - to, -126));
+            cv = to;
           }
           df = max(e - cv, -60);
         }

@@ -112,6 +112,42 @@ def test_key_tiles_of_zeros_and_bad_blocks_with_small_queries(qmul, scale, n, dt
     close(out, o, to, "out")
 
 
+# ------------------------------------------------------------------ value rows of very different sizes
+
+def weighted(g, L, Hkv, d, powers):
+    """Keys whose scores against the query (1, 0, 0, ...) at scale 1 are powers * ln 2."""
+    k = torch.zeros(L, Hkv, d, device="cuda")
+    k[..., 0] = powers[:, None] * LN2
+    return k
+
+
+def unit_queries(n, Hq, d, dtype):
+    q = torch.zeros(n, Hq, d, dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    return q
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 4, 60, 300])
+@pytest.mark.parametrize("order", ["large first", "small first", "turns", "rising", "falling"])
+@pytest.mark.parametrize("small, large, low", [(2.0 ** -20, 2.0 ** 20, -60.0), (2.0 ** -9, 2.0 ** 9, -40.0),
+                                               (2.0 ** -15, 2.0 ** 24, -100.0), (1.0, 2.0 ** 40, -90.0)])
+def test_tiles_of_small_values_beside_tiles_of_large_ones(small, large, low, order, n, dtype, bits):
+    """Tiles whose values differ by up to 2^40, the large ones of hardly any weight: the outputs are the small ones'."""
+    g = gen(204)
+    L, Hq, Hkv, d, tile = 1600, 8, 2, 64, 128
+    at = torch.arange(L, device="cuda") // tile
+    last = int(at[-1])
+    frac = {"large first": (at < 3).float(), "small first": ((at >= 5) & (at < 9)).float(), "turns": (at % 2 == 0).float(),
+            "rising": at.float() / last, "falling": 1 - at.float() / last}[order]
+    frac[L - 301:] = frac[L - 301:] * 0 + float(frac[L - 302])  # (every new token sees both kinds before it)
+    powers = low * frac + 0.5 * torch.randn(L, generator=g, device="cuda")
+    f = small * (large / small) ** frac.round(decimals=1)
+    v = randn(g, L, Hkv, d) * f[:, None, None]
+    pool, table = pool_of([(weighted(g, L, Hkv, d, powers), v)], 64, Hq, dtype, bits, g)
+    check(pool, table, [L], [n], unit_queries(n, Hq, d, dtype), 1.0)
+
+
 # ------------------------------------------------------------------ NaN behind a query
 
 @pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 0), (F32, 8)])
