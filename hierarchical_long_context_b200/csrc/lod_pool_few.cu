@@ -50,10 +50,16 @@ struct FewSmem {
 // taken against a reference maximum per query row; only when some score
 // exceeds it by more than 2^8 (and on a unit's first tile) does the
 // warpgroup find new maxima and rescale O^T.
-// With an 8-bit pool the weight of a key carries its value row's exponent,
-// w = 2^(score + e_v - m) with m the running maximum of score + e_v: the
-// codes then enter the MMA as they are, and w fills f16's range from the top,
-// so what f16 drops lies 2^-30 below the largest weighted value.
+// With an 8-bit pool the weight of a key carries its value row's exponent e_v
+// relative to cv, that of the warpgroup's first tile: w = 2^(score + dv - m),
+// dv = e_v - cv, with m the running maximum of score + dv.  The codes then
+// enter the MMA as they are, and w fills f16's range from the top, so what
+// f16 drops lies 2^-30 below the largest weighted value.  The sums take
+// w 2^-dv, and so need w in fp32's range: dv is held above -60 (a row smaller
+// than that takes the rest as a factor behind the exponential; rows of zeros
+// are the common case), and when a row comes 2^30 above cv the warpgroup
+// takes a new one.  The sums then stay below 2^66 of a weight's unit by m
+// being held high enough.
 // Roles: warp 0 copies of keys, warp 1 the MMAs of S^T, warp 2 those of O^T
 // (two issuers: neither waits for the other's operands), warp 3 query tiles
 // and copies of values, warps 4-7 and 8-11 the softmax of even and odd tiles,
@@ -76,6 +82,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
   constexpr float kTau = 8.f;
   constexpr float kUp = 6.f;  // 8-bit: weights are up to 2^14 of f16's 2^16
+  constexpr float kDvMin = -60.f, kDvMax = 30.f, kSumMax = 66.f;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -362,7 +369,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more(); w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
       const float* qe = qe_s + (k & 15) * NQ;
-      float cv = 0.f;  // (8-bit) a value exponent of the unit: sums of weights are in units of 2^cv
+      float cv = 0.f;  // (8-bit) the value exponent that O^T is in units of
       const int p0 = (int)(w.s.len - w.s.n), g0 = (int)w.u.i * RQ;
       const int pos_lo = p0 + g0 / a.G, pos_hi = p0 + (g0 + w.nrow - 1) / a.G;
       auto first_of = [&](int p) { return a.window > 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0; };
@@ -387,13 +394,15 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         const uint32_t ok = info_s[c & 15];
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
         bool live = true;
-        float ks = a.scale_log2, ve = 0.f;
+        float ks = a.scale_log2, ve = 0.f, dv = 0.f;
         if constexpr (Q8) {
           // (rows of exponent 255 hold NaN codes: any factor will do)
           const int e0 = ex_s[(c & 15) * 256 + r], e1 = ex_s[(c & 15) * 256 + 128 + r];
           ks *= exp2i(e0 == 255 ? 0 : max(e0, 7) - 127);
-          ve = (float)(e1 == 255 ? 0 : max(e1, 7) - 127);
+          ve = e1 == 255 ? -INFINITY : (float)(max(e1, 7) - 127);
         }
+        auto relative = [&] { dv = ve == -INFINITY ? 0.f : fminf(fmaxf(ve - cv, kDvMin), kDvMax); };
+        if (Q8) relative();
         if (masked) {
           live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
           // (a barrier's parity tells a phase only from the one before it: with
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           float v[CH];
           load_cols(ts + n0, v);
 #pragma unroll
-          for (int n = 0; n < CH; ++n) y[n0 + n] = Q8 ? fmaf(v[n], ks * qe[n0 + n], ve) : v[n] * ks;
+          for (int n = 0; n < CH; ++n) y[n0 + n] = v[n] * (Q8 ? ks * qe[n0 + n] : ks);
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -429,31 +438,40 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
             y[n] = live && t >= fl.x && t <= fl.y ? y[n] : -INFINITY;
           }
         }
-        bool grow = j == j0 || !go;
+        bool grow = j == j0 || !go || (Q8 && live && ve > cv + kDvMax);
+        const float tau = kTau - dv;
 #pragma unroll
         for (int n = 0; n < RQ; n += 4) {
           const float4 mr = *reinterpret_cast<const float4*>(mine_m + n);
-          grow |= y[n] > mr.x + kTau || y[n + 1] > mr.y + kTau || y[n + 2] > mr.z + kTau || y[n + 3] > mr.w + kTau;
+          grow |= y[n] > mr.x + tau || y[n + 1] > mr.y + tau || y[n + 2] > mr.z + tau || y[n + 3] > mr.w + tau;
         }
         if (bar_red_or(bar_or, 128, grow)) {
           go = !bar_red_or(bar_or, 128, !go);
           if (!go) break;
+          float up = 0.f;  // what cv grows by
+          if constexpr (Q8) {
+            const float top = warp_max(live ? ve : -INFINITY);
+            if (lane == 0) top_s[half * 4 + q4] = top;
+            bar_named_sync(bar_wg, 128);
+            const float x = fmaxf(fmaxf(top_s[half * 4], top_s[half * 4 + 1]), fmaxf(top_s[half * 4 + 2], top_s[half * 4 + 3]));
+            if (j == j0) {
+              cv = x == -INFINITY ? 0.f : x;
+            } else if (x > cv + kDvMax) {
+              up = x - cv;
+              cv = x;
+            }
+            relative();
+          }
           // new maxima: over the warp's keys, then over the four warps (the
           // sums of tile c - 2 are complete: waited for above)
 #pragma unroll
           for (int n = 0; n < RQ; ++n) {
-            const float x = warp_max(y[n]);
+            float x = y[n] + dv;
+            if (Q8 && up > 0.f && l[n] > 0.f) x = fmaxf(x, mine_m[n] + log2f(l[n]) - kSumMax);
+            x = warp_max(x);
             if (lane == n % 32) red[q4 * 64 + n] = x;
           }
-          if (Q8 && j == j0) {
-            const float x = warp_max(live ? ve : -INFINITY);
-            if (lane == 0) top_s[half * 4 + q4] = x;
-          }
           bar_named_sync(bar_wg, 128);
-          if (Q8 && j == j0) {
-            const float x = fmaxf(fmaxf(top_s[half * 4], top_s[half * 4 + 1]), fmaxf(top_s[half * 4 + 2], top_s[half * 4 + 3]));
-            cv = x == -INFINITY ? 0.f : x;
-          }
 #pragma unroll
           for (int n0 = 0; n0 < RQ; n0 += 8) {
             float f[8];
@@ -461,9 +479,10 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
             for (int n = 0; n < 8; ++n) {
               const int q = n0 + n;
               const float x = fmaxf(fmaxf(red[q], red[64 + q]), fmaxf(red[128 + q], red[192 + q]));
-              const float m = mine_m[q];
-              f[n] = x > m ? (m == -INFINITY ? 0.f : ex2_approx(m - x)) : 1.f;
-              l[q] *= f[n];
+              // (up moves the maxima's unit: O^T in it falls, the sums do not)
+              const float m = mine_m[q], mn = fmaxf(x, m - up);
+              f[n] = m == -INFINITY ? 0.f : mn > m - up ? ex2_approx(m - up - mn) : 1.f;
+              l[q] *= up > 0.f && m != -INFINITY ? ex2_approx(m - mn) : f[n];
             }
             if (j > j0) {
               float o[8];
@@ -475,11 +494,14 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           }
           bar_named_sync(bar_wg, 128);  // every thread has read the old maxima
           if (r < RQ)
-            mine_m[r] = fmaxf(fmaxf(fmaxf(red[r], red[64 + r]), fmaxf(red[128 + r], red[192 + r])), mine_m[r]);
+            mine_m[r] = fmaxf(fmaxf(fmaxf(red[r], red[64 + r]), fmaxf(red[128 + r], red[192 + r])), mine_m[r] - up);
           bar_named_sync(bar_wg, 128);
         }
         // weights
-        const float pe = exp2i(min(max((int)(cv - ve), -126), 126));
+        // (8-bit) to the sums' unit, and what dv lacks of the row's exponent
+        const float pe = Q8 ? exp2i(-(int)dv) : 1.f;
+        const float pv = Q8 && ve != -INFINITY ? exp2i((int)fminf(fmaxf(ve - cv - dv, -126.f), 0.f)) : 1.f;
+        const float dk = dv + kUp;
         unsigned char* P = sm + S::off_P + (size_t)half * S::kP + (r >> 6) * NQ * 128 + (r & 7) * 2;
         const int ch = (r & 63) >> 3;
 #pragma unroll
@@ -488,10 +510,10 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           const float mr[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]) + (Q8 ? kUp : 0.f));
+            const float p = ex2_approx(y[n + q] - (mr[q] == -INFINITY ? 0.f : mr[q]) + (Q8 ? dk : 0.f));
             l[n + q] = Q8 ? fmaf(p, pe, l[n + q]) : l[n + q] + p;
             *reinterpret_cast<uint16_t*>(P + (n + q) * 128 + ((ch ^ ((n + q) & 7)) << 4)) =
-                Q8 ? (uint16_t)pack_f16x2(p, 0.f) : (uint16_t)pack_bf16x2(p, 0.f);
+                Q8 ? (uint16_t)pack_f16x2(p * pv, 0.f) : (uint16_t)pack_bf16x2(p, 0.f);
           }
         }
         tc::fence_proxy_async();
@@ -510,8 +532,8 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         if (lane == n % 32) red[q4 * 64 + n] = x;
       }
       bar_named_sync(bar_wg, 128);
-      // 8-bit: O^T is in units of 2^(m - kUp), the sums of 2^(m - kUp - cv)
-      const float dm = Q8 ? kUp + cv : 0.f;
+      // 8-bit: the sums are in units of 2^(m - kUp), O^T of 2^(m - kUp + cv)
+      const float dm = Q8 ? kUp : 0.f;
       float2* fin_s = reinterpret_cast<float2*>(sm + S::off_fin);
       const float up = Q8 ? exp2i((int)cv) : 1.f;
       if (half == 1) {

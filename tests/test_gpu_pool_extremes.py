@@ -128,6 +128,23 @@ def unit_queries(n, Hq, d, dtype):
 
 
 @pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 2, 4, 60])
+@pytest.mark.parametrize("size", [300.0, 2.0 ** 15, 2.0 ** 40, 2.0 ** -20])
+@pytest.mark.parametrize("where", ["first", "last", "spread"])
+def test_keys_of_zero_values_keep_their_weight(where, size, n, dtype, bits):
+    """Most value rows are zeros; a few are large, and their scores 10 to 14 powers of two above the rest."""
+    g = gen(203)
+    L, Hq, Hkv, d = 6000, 8, 1, 128
+    powers = torch.randn(L, generator=g, device="cuda") - 2
+    v = torch.zeros(L, Hkv, d, device="cuda")
+    top = {"first": torch.arange(3, 9), "last": torch.arange(L - 70, L - 64), "spread": torch.arange(700, L - 700, 900)}[where]
+    powers[top] = 10 + 4 * torch.rand(len(top), generator=g, device="cuda")
+    v[top] = size * (1 + 0.4 * torch.rand(len(top), Hkv, d, generator=g, device="cuda"))
+    pool, table = pool_of([(weighted(g, L, Hkv, d, powers), v)], 32, Hq, dtype, bits, g)
+    check(pool, table, [L], [n], unit_queries(n, Hq, d, dtype), 1.0)
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
 @pytest.mark.parametrize("n", [1, 4, 60, 300])
 @pytest.mark.parametrize("order", ["large first", "small first", "turns", "rising", "falling"])
 @pytest.mark.parametrize("small, large, low", [(2.0 ** -20, 2.0 ** 20, -60.0), (2.0 ** -9, 2.0 ** 9, -40.0),
