@@ -138,6 +138,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _check_lens(seq_lens, B: int):
+    """The kernels read B int64 values in a row: an expanded or strided view would give them others."""
+    if seq_lens.shape != (B,) or seq_lens.dtype is not torch.int64 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int64 [B] tensor")
+
+
 def lod_build_index(params: Params, K, V, chunk_begin: int, chunk_end: int, index: Index, ws=None,
                     stream=None) -> None:
     """Build chunks [chunk_begin, chunk_end) of every (b, kvh) sequence."""
@@ -160,6 +166,7 @@ def lod_append_kv(params: Params, K, V, seq_lens, k_new, v_new, stream=None) -> 
     for t in (k_new, v_new):
         if t.shape != shape or t.dtype != params.dtype or not t.is_contiguous():
             raise ValueError("k_new / v_new must be contiguous %s %s" % (shape, params.dtype))
+    _check_lens(seq_lens, params.B)
     check("lod_append_kv", lib.lod_append_kv(
         ctypes.byref(params.c()), _ptr(K), _ptr(V), st, _ptr(seq_lens), _ptr(k_new), _ptr(v_new),
         _stream(stream)))
@@ -172,7 +179,8 @@ def lod_build_ready(params: Params, K, V, seq_lens, index: Index, ws=None, strea
     every decode step, e.g. on a second stream."""
     lib = load()
     st = _kv_strides(params, K, V)
-    if seq_lens.shape != (params.B,) or seq_lens.dtype != torch.int64 or seq_lens.device != K.device:
+    _check_lens(seq_lens, params.B)
+    if seq_lens.device != K.device:
         raise ValueError("seq_lens must be int64 [B] on the cache's device")
     if ws is None:
         ws = workspace(params, _lib.LOD_OP_BUILD, K.device)
@@ -191,7 +199,8 @@ def lod_decode(params: Params, q, K, V, seq_lens, index: Index, out=None, lse=No
     st = _kv_strides(params, K, V)
     if q.shape != (params.B, params.Hq, params.d) or q.dtype != params.dtype or not q.is_contiguous():
         raise ValueError("q must be contiguous [B, Hq, d] of the cache dtype")
-    if seq_lens.dtype != torch.int64 or seq_lens.shape != (params.B,) or not seq_lens.is_cuda:
+    _check_lens(seq_lens, params.B)
+    if not seq_lens.is_cuda:
         raise ValueError("seq_lens must be a device int64 tensor [B]")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=K.device)
@@ -365,8 +374,7 @@ def lod_append_rope(params: Params, rope: Rope, q, k, v, K, V, seq_lens, q_out=N
     ks = _rows(k, (B, Hkv, n, d), dt, "k")
     if _rows(v, (B, Hkv, n, d), dt, "v") is not ks and v.stride() != k.stride():
         raise ValueError("k and v must share strides")
-    if seq_lens.shape != (B,) or seq_lens.dtype is not torch.int64:
-        raise ValueError("seq_lens must be int64 [B]")
+    _check_lens(seq_lens, B)
     qs = os = None
     if q is not None:
         shape = (B, params.Hq, n, d)

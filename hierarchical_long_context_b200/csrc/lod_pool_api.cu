@@ -154,6 +154,7 @@ int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q
   if (rc) return rc;
   if (!rope) return fail(LOD_EINVAL, "rope is NULL");
   if (!seq_lens) return fail(LOD_EINVAL, "seq_lens must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(seq_lens) & 7u) return fail(LOD_EINVAL, "seq_lens must be 8-byte aligned");
   if (n_new < 1 || n_new > p->Tmax) return fail(LOD_EINVAL, "n_new = %lld must be in [1, Tmax]", (long long)n_new);
   const int64_t elem = elem_of(p->dtype);
   const int64_t N = p->B * n_new;
