@@ -244,7 +244,16 @@ def _strides(st: tuple):
     return (ctypes.c_int64 * len(st))(*st)
 
 
-class Rope:
+class _Fixed:
+    """Its attributes stay as they were made: the C struct is filled from them once, and the calls' checks read them."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__ and name in self.__dict__:
+            raise AttributeError("%s.%s is fixed; make another %s" % (type(self).__name__, name, type(self).__name__))
+        super().__setattr__(name, value)
+
+
+class Rope(_Fixed):
     """Norm and rotation of query and key rows (lod_rope).  inv_freq: float32 [rot / 2] on the device (None: no
     rotation); q_norm, k_norm: [d] weights of the rows' dtype (None: no norm of those rows)."""
 
@@ -258,20 +267,20 @@ class Rope:
         self.inv_freq, self.q_norm, self.k_norm = inv_freq, q_norm, k_norm
         self._c = _lib.lod_rope(_addr(q_norm), _addr(k_norm), _addr(inv_freq), eps,
                                 0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), 0)
+        self._fits = [None]  # the (d, dtype) the weights were last checked against
         self._ref = ctypes.byref(self._c)
-        self._fits = None  # the (d, dtype) the weights were last checked against
 
     def ref(self, d: int, dtype: torch.dtype):
         """The C struct, after checking the weights against the rows they are for."""
-        if self._fits != (d, dtype):
+        if self._fits[0] != (d, dtype):
             for w in (self.q_norm, self.k_norm):
                 if w is not None and (w.shape[0] != d or w.dtype != dtype):
                     raise ValueError("norm weights must be [%d] %s" % (d, dtype))
-            self._fits = (d, dtype)
+            self._fits[0] = (d, dtype)
         return self._ref
 
 
-class Pool:
+class Pool(_Fixed):
     """A block pool (lod_pool) over the caller's tensors: K, V [blocks, Hkv, block, d] in dtype, or with Ke, Ve
     (uint8 [blocks, Hkv, block]) as e4m3 codes (float8_e4m3fn or uint8)."""
 
@@ -312,7 +321,7 @@ class Pool:
         return self._c.bits
 
 
-class PoolBatch:
+class PoolBatch(_Fixed):
     """The sequences of a call (lod_batch): block_table int32 [B, max_blocks], seq_lens int64 [B], new_begin int64
     [B + 1], all on the device; tokens: packed rows N of the call; max_new: most new tokens of one sequence."""
 

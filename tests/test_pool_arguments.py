@@ -37,3 +37,21 @@ def test_lengths_that_are_no_row_of_int64_are_refused(lens):
 
 def test_misaligned_lengths_are_refused():
     assert _append(lens=FAKE + 4) == _lib.LOD_EINVAL and "seq_lens" in err()
+
+
+@pytest.mark.parametrize("name, value", [("tokens", 2), ("max_new", 5), ("B", 1), ("block_table", None), ("seq_lens", None)])
+def test_a_batch_is_fixed(name, value):
+    """The checks read the attributes and the kernels the C struct: 1 packed row checked, 3 written."""
+    b = _cpu_batch()
+    with pytest.raises(AttributeError, match=name):
+        setattr(b, name, value)
+    assert getattr(b, name) is not value and b._c.N == 3
+
+
+def test_a_pool_and_a_rope_are_fixed():
+    p, r = _cpu_pool(), api.Rope(torch.zeros(32))
+    for obj, name in ((p, "K"), (p, "Hq"), (p, "d"), (p, "dtype"), (r, "inv_freq"), (r, "q_norm")):
+        with pytest.raises(AttributeError, match=name):
+            setattr(obj, name, None)
+    r.ref(64, torch.bfloat16)
+    r.ref(128, torch.float32)
