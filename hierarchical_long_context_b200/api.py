@@ -7,6 +7,7 @@ pointers.  All arithmetic runs in liblod.so.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
@@ -138,6 +139,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _made_on(stream):
+    """Where a call makes the buffers that its caller left out: on the stream that uses them, so that their zero fill
+    comes before the kernels and their memory is not handed out again while those run."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _check_lens(seq_lens, B: int):
     """The kernels read B int64 values in a row: an expanded or strided view would give them others."""
     if seq_lens.shape != (B,) or seq_lens.dtype is not torch.int64 or not seq_lens.is_contiguous():
@@ -150,7 +157,8 @@ def lod_build_index(params: Params, K, V, chunk_begin: int, chunk_end: int, inde
     lib = load()
     st = _kv_strides(params, K, V)
     if ws is None:
-        ws = workspace(params, _lib.LOD_OP_BUILD, K.device)
+        with _made_on(stream):
+            ws = workspace(params, _lib.LOD_OP_BUILD, K.device)
     check("lod_build_index", lib.lod_build_index(
         ctypes.byref(params.c()), _ptr(K), _ptr(V), st, chunk_begin, chunk_end,
         ctypes.byref(index.c()), _ptr(ws), ws.numel(), _stream(stream)))
@@ -183,7 +191,8 @@ def lod_build_ready(params: Params, K, V, seq_lens, index: Index, ws=None, strea
     if seq_lens.device != K.device:
         raise ValueError("seq_lens must be int64 [B] on the cache's device")
     if ws is None:
-        ws = workspace(params, _lib.LOD_OP_BUILD, K.device)
+        with _made_on(stream):
+            ws = workspace(params, _lib.LOD_OP_BUILD, K.device)
     check("lod_build_ready", lib.lod_build_ready(
         ctypes.byref(params.c()), _ptr(K), _ptr(V), st, _ptr(seq_lens), ctypes.byref(index.c()),
         _ptr(ws), ws.numel(), _stream(stream)))
@@ -203,9 +212,11 @@ def lod_decode(params: Params, q, K, V, seq_lens, index: Index, out=None, lse=No
     if not seq_lens.is_cuda:
         raise ValueError("seq_lens must be a device int64 tensor [B]")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=K.device)
+        with _made_on(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=K.device)
     if ws is None:
-        ws = workspace(params, _lib.LOD_OP_DECODE, K.device)
+        with _made_on(stream):
+            ws = workspace(params, _lib.LOD_OP_DECODE, K.device)
     check("lod_decode", lib.lod_decode(
         ctypes.byref(params.c()), _ptr(q), _ptr(K), _ptr(V), st, _ptr(seq_lens),
         ctypes.byref(index.c()), _ptr(out), _ptr(lse), _ptr(sel_groups), _ptr(sel_pages), _ptr(ws),
@@ -223,9 +234,11 @@ def lod_prefill(params: Params, q, q_begin: int, K, V, index: Index, out=None, l
             or q.dtype != params.dtype or not q.is_contiguous():
         raise ValueError("q must be contiguous [B, Hq, Tq, d] of the cache dtype")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=K.device)
+        with _made_on(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=K.device)
     if ws is None:
-        ws = workspace(params, _lib.LOD_OP_PREFILL, K.device)
+        with _made_on(stream):
+            ws = workspace(params, _lib.LOD_OP_PREFILL, K.device)
     check("lod_prefill", lib.lod_prefill(
         ctypes.byref(params.c()), _ptr(q), q_begin, q.shape[2], _ptr(K), _ptr(V), st,
         ctypes.byref(index.c()), _ptr(out), _ptr(lse), _ptr(sel_groups), _ptr(sel_pages), _ptr(ws),
@@ -389,7 +402,8 @@ def lod_append_rope(params: Params, rope: Rope, q, k, v, K, V, seq_lens, q_out=N
         shape = (B, params.Hq, n, d)
         qs = _rows(q, shape, dt, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=K.device)
+            with _made_on(stream):
+                q_out = torch.empty(shape, dtype=dt, device=K.device)
         os = _rows(q_out, shape, dt, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -413,7 +427,8 @@ def lod_pool_append(pool: Pool, batch: PoolBatch, k, v, rope: Rope | None = None
     if q is not None:
         qs = _rows(q, (N, pool.Hq, d), dt, "q")
         if q_out is None:
-            q_out = torch.empty(N, pool.Hq, d, dtype=dt, device=pool.K.device)
+            with _made_on(stream):
+                q_out = torch.empty(N, pool.Hq, d, dtype=dt, device=pool.K.device)
         os = _rows(q_out, (N, pool.Hq, d), dt, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -457,18 +472,21 @@ def pool_workspace(pool: Pool, batch: PoolBatch) -> torch.Tensor:
 def lod_pool_attend(pool: Pool, batch: PoolBatch, q, out=None, lse=None, window: int = 0, scale: float = 0.0,
                     ws=None, stream=None):
     """Exact causal attention of the new tokens' q [N, Hq, d] over the pool (which already holds them); window > 0
-    limits each query to its last `window` keys; lse float32 [N, Hq].  Returns out."""
+    limits each query to its last `window` keys; lse float32 [N, Hq].  Returns out.  The status word (refused
+    sequences, bad blocks) is the first of `ws`; without ws it is lost with the call's own workspace."""
     if batch.new_begin is None:
         raise ValueError("the batch has no new_begin")
     shape = (batch.tokens, pool.Hq, pool.d)
     qs = _rows(q, shape, pool.dtype, "q")
     if out is None:
-        out = torch.empty(shape, dtype=pool.dtype, device=pool.device)
+        with _made_on(stream):
+            out = torch.empty(shape, dtype=pool.dtype, device=pool.device)
     os = _rows(out, shape, pool.dtype, "out")
     if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [N, Hq] tensor")
     if ws is None:
-        ws = pool_workspace(pool, batch)
+        with _made_on(stream):
+            ws = pool_workspace(pool, batch)
     check("lod_pool_attend", load().lod_pool_attend(
         pool._ref, batch._ref, q.data_ptr(), qs, out.data_ptr(), os, _addr(lse), window, scale, ws.data_ptr(),
         ws.numel() * ws.element_size(), _stream_handle(stream, pool.device)))
