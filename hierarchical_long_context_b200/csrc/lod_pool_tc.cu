@@ -447,10 +447,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 t = ffma2(make_float2(y[32 * q + 2 * e], y[32 * q + 2 * e + 1]), sc2, mu2);
-              // the exponentials are shared out: the special-function unit
-              // takes 8 cycles for a warp's 32, the FMA pipe 7 (3 of 8 on the
-              // FMA pipe 4.21 ms for 2048 tokens over 128K, 2 of 8 4.20, 4 of 8 4.33)
-              if (e % 8 == 1 || e % 8 == 3 || e % 8 == 6) {
+              // the exponentials are shared out between the special-function
+              // unit and the FMA pipe (2 of 8 there: 2048 tokens over 128K
+              // 4.29 ms, the mixed 8-bit batch of nine sequences 72.0 us; 3 of
+              // 8 4.34 and 73.4, 1 of 8 4.33 and 72.5)
+              if (e % 8 == 2 || e % 8 == 6) {
                 t = exp2_fma2(t);
               } else {
                 t.x = ex2_approx(t.x);

@@ -36,9 +36,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // 2^x of a pair on the FMA pipe, for x <= 128 (0 below -127; not for NaN): x =
 // n + f with n the nearest integer (the sum with 1.5 * 2^23 leaves it in the
-// low bits), a polynomial of degree 4 for 2^f on [-1/2, 1/2], n added to its
+// low bits), a polynomial of degree 5 for 2^f on [-1/2, 1/2], n added to its
 // exponent.  The coefficients minimise the largest relative error with
-// p(0) = 1 (a linear programme over a grid): 2.9e-6, 2e-7 on average.
+// p(0) = 1 (a linear programme over a grid): 8.1e-8, 1.6e-7 with the fp32
+// roundings (degree 4: 2.9e-6, more than the bound on a weight allows).
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
   constexpr float kMagic = 12582912.f;
   x.x = fmaxf(x.x, -127.f);
@@ -46,10 +47,12 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
   const float2 t = fadd2(x, make_float2(kMagic, kMagic));
   const float2 n = fadd2(t, make_float2(-kMagic, -kMagic));
   const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);
-  float2 p = make_float2(0.009585382416844368f, 0.009585382416844368f);
-  p = ffma2(p, f, make_float2(0.05590662732720375f, 0.05590662732720375f));
-  p = ffma2(p, f, make_float2(0.24024038016796112f, 0.24024038016796112f));
-  p = ffma2(p, f, make_float2(0.6931241750717163f, 0.6931241750717163f));
+  constexpr float c5 = 0.0013274633092805743f, c4 = 0.009671961888670921f, c3 = 0.055506784468889236f,
+                  c2 = 0.24022234976291656f, c1 = 0.6931470632553101f;
+  float2 p = ffma2(make_float2(c5, c5), f, make_float2(c4, c4));
+  p = ffma2(p, f, make_float2(c3, c3));
+  p = ffma2(p, f, make_float2(c2, c2));
+  p = ffma2(p, f, make_float2(c1, c1));
   p = ffma2(p, f, make_float2(1.f, 1.f));
   p.x = __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23));
   p.y = __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23));
