@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(1024) pool_plan_kernel(PoolAttendArgs a) {
       int64_t n = 0;
       if (b < B && a.RT[b + 1] > a.RT[b]) {
         const SeqView s = seq_view(a.batch, a.pool.shift, b);
-        n = a.window > 0 && s.len > a.window + s.n ? a.window + s.n : s.len;
+        n = a.window > 0 && s.len - s.n > a.window ? a.window + s.n : s.len;
       }
       block_scan<false>(n, ws, &total);
       keys += total;

@@ -136,3 +136,15 @@ def test_batches_of_many_sequences(falls, G, B, dtype, bits):
         down = begin[at] // 2
         begin = begin[:at] + [x - down for x in begin[at:]]
     walk(begin, lens, N, 3, G, 1, 64, 16, dtype, bits, 103)
+
+
+def test_a_window_as_long_as_any_is_no_window():
+    """The list of a cache beyond L2 is cut the same way, so the bits are the same."""
+    L, n = 40000, 2048
+    g = gen(104)
+    pool, table = make_pool(g, [L], 64, 16, 8, 128, BF, 0)
+    batch = api.PoolBatch(table, torch.tensor([L], device="cuda"), torch.tensor([0, n], device="cuda"), tokens=n, max_new=n)
+    q = randn(g, n, 16, 128, dtype=BF)
+    want = lod.lod_pool_attend(pool, batch, q)
+    for window in (L, 1 << 40, (1 << 63) - n, (1 << 63) - 1):
+        assert torch.equal(lod.lod_pool_attend(pool, batch, q, window=window), want), window
