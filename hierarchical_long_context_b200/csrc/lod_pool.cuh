@@ -135,6 +135,19 @@ __device__ __forceinline__ SeqView seq_view(const BatchView& bt, int shift, int 
   return s;
 }
 
+// The same of a sequence that the work list holds, and so is known to be good:
+// every role of a CTA walks the list, and the checks in each of them cost
+// instruction cache.
+__device__ __forceinline__ SeqView seq_taken(const BatchView& bt, int b) {
+  SeqView s;
+  s.r0 = bt.begin[b];
+  s.r1 = bt.begin[b + 1];
+  s.len = bt.seq_lens[b];
+  s.n = (int)(s.r1 - s.r0);
+  s.ok = true;
+  return s;
+}
+
 // Key tiles [lo, hi) that row tile i (rows [i * TM, ...)) of a sequence reads.
 template <int TM, int KT>
 __device__ __forceinline__ void row_tile_keys(const SeqView& s, int G, int64_t window, int64_t i, int& lo, int& hi) {
@@ -182,7 +195,7 @@ __device__ __forceinline__ Unit find_unit(const PoolAttendArgs& a, const int64_t
     u.i = l;
     u.begin = head0 + pre[l];
   }
-  const SeqView s = seq_view(a.batch, a.pool.shift, u.b);
+  const SeqView s = seq_taken(a.batch, u.b);
   row_tile_keys<TM, KT>(s, a.G, a.window, u.i, u.lo, u.hi);
   return u;
 }
@@ -222,7 +235,7 @@ struct Walk {
     w1 = w0 + share < total ? w0 + share : total;
     if (w < w1) {
       u = find_unit<TM, KT>(a, Wb, w);
-      s = seq_view(a.batch, a.pool.shift, u.b);
+      s = seq_taken(a.batch, u.b);
       nt = (s.n * a.G + TM - 1) / TM;
       piece();
       if (kt0 == kt1) next();
@@ -249,8 +262,8 @@ struct Walk {
         if (++u.h == a.pool.Hkv) {
           u.h = 0;
           do ++u.b;
-          while (Wb[u.b + 1] == Wb[u.b]);  // (no new tokens, or refused)
-          s = seq_view(a.batch, a.pool.shift, u.b);
+          while (Wb[u.b + 1] == u.begin);  // (no new tokens, or refused)
+          s = seq_taken(a.batch, u.b);
           nt = (s.n * a.G + TM - 1) / TM;
         }
       }
@@ -276,30 +289,29 @@ struct Walk {
 constexpr int kInlineSeqs = 256;
 
 // Wb of sequences with one row tile each, by the whole CTA (at least one
-// warp); ends with a CTA barrier.  While new_begin rises no entry lies above a
-// later one; the running maximum is taken only once it has fallen.
+// warp); ends with a CTA barrier.  The sequences are read side by side, then
+// added up by a warp.  While new_begin rises no entry lies above a later one;
+// the running maximum is taken only where it falls.
 template <int TM, int KT>
 __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb) {
+  bool falls = false;
+  for (int b = threadIdx.x; b < a.batch.B; b += blockDim.x) {
+    const SeqView s = seq_view(a.batch, a.pool.shift, b);
+    int lo = 0, hi = -kUnitCost;
+    if (s.n > 0) row_tile_keys<TM, KT>(s, a.G, a.window, 0, lo, hi);
+    Wb[b + 1] = (int64_t)(hi - lo + kUnitCost) * a.pool.Hkv;
+    falls |= s.r1 < s.r0;
+  }
+  falls = __syncthreads_or(falls);
   if (threadIdx.x < 32) {
     int64_t at = 0, top = INT64_MIN;
-    bool fell = false;
     if (threadIdx.x == 0) Wb[0] = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch.B; b0 += 32) {
       const int b = b0 + threadIdx.x;
-      int64_t n = 0, r0 = INT64_MIN;
-      bool falls = false;
-      if (b < a.batch.B) {
-        const SeqView s = seq_view(a.batch, a.pool.shift, b);
-        r0 = s.r0;
-        falls = s.r1 < s.r0;
-        if (s.n > 0) {
-          int lo, hi;
-          row_tile_keys<TM, KT>(s, a.G, a.window, 0, lo, hi);
-          n = (int64_t)(hi - lo + kUnitCost) * a.pool.Hkv;
-        }
-      }
-      fell |= __any_sync(0xffffffffu, falls) != 0;
-      if (fell) {
+      int64_t n = b < a.batch.B ? Wb[b + 1] : 0;
+      if (falls) {
+        const int64_t r0 = b < a.batch.B ? a.batch.begin[b] : INT64_MIN;
         int64_t m = r0 > top ? r0 : top;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -321,42 +333,55 @@ __device__ __forceinline__ void plan_inline(const PoolAttendArgs& a, int64_t* Wb
   __syncthreads();
 }
 
-// Rows of refused sequences: out = 0, lse = -inf.  Every CTA of the grid calls
-// this with all its threads; the CTAs share the sequences out.  A refused
-// sequence may name rows of another that is not: of its rows it clears those
-// that no earlier sequence reaches.  (The entries of new_begin up to b rise
-// and fall from begin[0] to their maximum, so each row between these two is
-// passed by a rising pair first: its sequence owns the row, or clears it.)
+// Rows of refused sequences: out = 0, lse = -inf.  A refused sequence may
+// name rows of another that is not: of its rows it clears those that no
+// earlier sequence reaches.  (The entries of new_begin up to b rise and fall
+// from begin[0] to their maximum, so each row between these two is passed by a
+// rising pair first: its sequence owns the row, or clears it.)
 template <typename T, int D>
-__device__ __forceinline__ void clear_refused(const PoolAttendArgs& a, const int64_t* Wb) {
+__device__ __forceinline__ void clear_rows(const PoolAttendArgs& a, int b) {
   constexpr int N16 = D * (int)sizeof(T) / 16;
+  const SeqView s = seq_view(a.batch, a.pool.shift, b);
+  if (s.ok && s.n == 0) return;
+  if (threadIdx.x == 0) set_status(a.status, LOD_ST_BAD_SEQLEN);
+  int64_t top = s.r0;
+  for (int i = threadIdx.x & 31; i < b; i += 32)
+    if (a.batch.begin[i] > top) top = a.batch.begin[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const int64_t x = __shfl_xor_sync(0xffffffffu, top, o);
+    if (x > top) top = x;
+  }
+  const int64_t end = s.r1 < a.batch.N ? s.r1 : a.batch.N, begin0 = a.batch.begin[0];
+#pragma unroll 1
+  for (int below = 0; below < 2; ++below) {  // its rows above every earlier entry, and those below the first one
+    int64_t r0 = below ? s.r0 : top;
+    const int64_t r1 = below && begin0 < end ? begin0 : end;
+    if (below && s.r0 >= begin0) break;
+    if (r0 < 0) r0 = 0;
+    for (int64_t x = threadIdx.x; r0 < r1 && x < (r1 - r0) * a.Hq * N16; x += blockDim.x) {
+      const int64_t row = x / N16, t = r0 + row / a.Hq, h = row % a.Hq;
+      const int c = (int)(x % N16);
+      reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.ot + h * a.oh)[c] = make_uint4(0, 0, 0, 0);
+      if (c == 0 && a.lse) a.lse[t * a.Hq + h] = -INFINITY;
+    }
+  }
+}
+// (the tensor-core kernels call it: inlined, it lengthens what every warp
+// fetches at its start, 1 us of a decode step; the fp32 kernel is 4 % slower
+// with a call in it)
+template <typename T, int D>
+__device__ __noinline__ void clear_rows_call(const PoolAttendArgs& a, int b) {
+  clear_rows<T, D>(a, b);
+}
+// Every CTA of the grid calls this with all its threads; the CTAs share the
+// sequences out.
+template <typename T, int D, bool kCall>
+__device__ __forceinline__ void clear_refused(const PoolAttendArgs& a, const int64_t* Wb) {
   for (int b = blockIdx.x; b < a.batch.B; b += gridDim.x) {
     if (Wb[b + 1] > Wb[b]) continue;
-    const SeqView s = seq_view(a.batch, a.pool.shift, b);
-    if (s.ok && s.n == 0) continue;
-    if (threadIdx.x == 0) set_status(a.status, LOD_ST_BAD_SEQLEN);
-    int64_t top = s.r0;
-    for (int i = threadIdx.x & 31; i < b; i += 32)
-      if (a.batch.begin[i] > top) top = a.batch.begin[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const int64_t x = __shfl_xor_sync(0xffffffffu, top, o);
-      if (x > top) top = x;
-    }
-    const int64_t end = s.r1 < a.batch.N ? s.r1 : a.batch.N, begin0 = a.batch.begin[0];
-#pragma unroll 1
-    for (int below = 0; below < 2; ++below) {  // its rows above every earlier entry, and those below the first one
-      int64_t r0 = below ? s.r0 : top;
-      const int64_t r1 = below && begin0 < end ? begin0 : end;
-      if (below && s.r0 >= begin0) break;
-      if (r0 < 0) r0 = 0;
-      for (int64_t x = threadIdx.x; r0 < r1 && x < (r1 - r0) * a.Hq * N16; x += blockDim.x) {
-        const int64_t row = x / N16, t = r0 + row / a.Hq, h = row % a.Hq;
-        const int c = (int)(x % N16);
-        reinterpret_cast<uint4*>(static_cast<T*>(a.out) + t * a.ot + h * a.oh)[c] = make_uint4(0, 0, 0, 0);
-        if (c == 0 && a.lse) a.lse[t * a.Hq + h] = -INFINITY;
-      }
-    }
+    if (kCall) clear_rows_call<T, D>(a, b);
+    else clear_rows<T, D>(a, b);
   }
 }
 

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(TM == 16 ? 128 : 256, 2) pool_simt_kernel(Pool
     plan_inline<TM, KT>(a, wb_s);
     Wb = wb_s;
   }
-  clear_refused<T, D>(a, Wb);
+  clear_refused<T, D, false>(a, Wb);
   Walk<TM, KT> w(a, Wb, blockIdx.x);
   for (; w.more(); w.next()) {
     const Unit& u = w.u;

@@ -51,15 +51,14 @@ struct FewSmem {
 // exceeds it by more than 2^8 (and on a unit's first tile) does the
 // warpgroup find new maxima and rescale O^T.
 // With an 8-bit pool the weight of a key carries its value row's exponent e_v
-// relative to cv, that of the warpgroup's first tile: w = 2^(score + dv - m),
-// dv = e_v - cv, with m the running maximum of score + dv.  The codes then
-// enter the MMA as they are, and w fills f16's range from the top, so what
-// f16 drops lies 2^-30 below the largest weighted value.  The sums take
-// w 2^-dv, and so need w in fp32's range: dv is held at or above -60 (a row
-// smaller than that takes the rest as a factor behind the exponential; rows of
-// zeros are the common case).  When a row comes 2^30 above cv the warpgroup
-// takes a new one, which moves the unit of m with it; the sums keep theirs
-// (2^(m + cv - cl)) but for a power of two that fits them.
+// relative to cv, the largest of the warpgroup's first tile: w = 2^(score + dv
+// - m), dv = e_v - cv, with m the running maximum of score + dv.  The codes
+// then enter the MMA as they are, and w fills f16's range from the top, so
+// what f16 drops lies 2^-30 below the largest weighted value.  The sums take
+// w 2^-dv, and so need w in fp32's range: dv is held at or above -60, and a
+// row smaller than that takes the rest as a factor behind the exponential
+// (rows of zeros are the common case; a first tile of nothing else has cv =
+// 0).
 // Roles: warp 0 copies of keys, warp 1 the MMAs of S^T, warp 2 those of O^T
 // (two issuers: neither waits for the other's operands), warp 3 query tiles
 // and copies of values, warps 4-7 and 8-11 the softmax of even and odd tiles,
@@ -82,8 +81,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   constexpr int NQ = S::NQ, KS = S::KS, VS = S::VS, RS = S::RS;
   constexpr float kTau = 8.f;
   constexpr float kUp = 6.f;  // 8-bit: weights are up to 2^14 of f16's 2^16
-  constexpr int kDvMin = -60, kDvMax = 30, kNoRow = -256;
-  constexpr int kSumMax = 66;
+  constexpr int kDvMin = -60, kDvMax = 126, kNoRow = -256;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -109,7 +107,6 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
   uint32_t* info_s = reinterpret_cast<uint32_t*>(sm + S::off_info);  // blocks that are there
   float* qe_s = reinterpret_cast<float*>(sm + S::off_qe);
   float* up_s = reinterpret_cast<float*>(const_cast<int*>(abort_s) + 1);
-  int* top_s = reinterpret_cast<int*>(up_s + 1);  // [2][4]
   unsigned char* ex_s = sm + S::off_ex;
   int64_t* wb_s = reinterpret_cast<int64_t*>(sm + S::off_wb);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -154,7 +151,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     plan_inline<RQ, kKT>(a, wb_s);
     Wb = wb_s;
   }
-  clear_refused<__nv_bfloat16, D>(a, Wb);
+  clear_refused<__nv_bfloat16, D, true>(a, Wb);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
     for (Walk<RQ, kKT> w(a, Wb, blockIdx.x); w.more(); w.next(), ++k) {
       const int T = w.kt1 - w.kt0;
       const float* qe = qe_s + (k & 15) * NQ;
-      int cv = 0, cl = 0;  // (8-bit) the value exponent that O^T is in units of, and the sums'
+      int cv = 0;  // (8-bit) the value exponent that O^T is in units of
       const int p0 = (int)(w.s.len - w.s.n), g0 = (int)w.u.i * RQ;
       const int pos_lo = p0 + g0 / a.G, pos_hi = p0 + (g0 + w.nrow - 1) / a.G;
       auto first_of = [&](int p) { return a.window > 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0; };
@@ -387,9 +384,11 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
       const int j0 = (c0 ^ half) & 1;  // this warpgroup's first tile of the unit
       for (int j = j0; j < T; j += 2) {
         const int c = c0 + j, k0 = (w.kt0 + j) * kKT, t = k0 + r;
-        // block mask and exponents first: what follows from them is ready when
-        // the scores are
-        go = __all_sync(0xffffffffu, wait_ring(ex_full, 16, c));
+        // (8-bit: the values too.  Conversion and softmax then take turns at the
+        // shared memory, which bounds both; side by side they measured 6 % more.)
+        go = __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) && wait_ring(ex_full, 16, c) &&
+                                         (!Q8 || wait_ring(vfull, VS, c)) && wait_ring(s_full, 2, c));
+        // (a failed wait is carried to the barrier below, where the four warps leave together)
         const uint32_t ok = info_s[c & 15];
         const bool masked = k0 + 127 > pos_lo || k0 < first_hi || ok != all_ok;
         bool live = true;
@@ -401,18 +400,23 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           ve = e1 == 255 ? kNoRow : max(e1, 7) - 127;
         }
         float dv = 0.f, pe = 1.f, pv = 1.f;  // (pe: a weight to the sums' unit; pv: what dv lacks of the row's exponent)
-        auto relative = [&] {
-          const int d = ve - cv, x = min(max(d, kDvMin), kDvMax);
-          dv = (float)x;
-          pe = exp2i(max(cl - cv - x, -126));
-          pv = ve == kNoRow ? 1.f : exp2i(min(max(d - x, -126), 0));
-        };
-        if (Q8) relative();
-        // (8-bit: the values too.  Conversion and softmax then take turns at the
-        // shared memory, which bounds both; side by side they measured 6 % more.)
-        go = go && __all_sync(0xffffffffu, (c < 2 || wait_ring(pv_done, 2, c - 2)) &&
-                                               (!Q8 || wait_ring(vfull, VS, c)) && wait_ring(s_full, 2, c));
-        // (a failed wait is carried to the barrier below, where the four warps leave together)
+        if constexpr (Q8) {
+          if (j == j0) {
+            // cv, by each warp from the tile's bytes: four a lane, those of
+            // NaN rows and behind the length left out
+            const uint32_t e4 = reinterpret_cast<const uint32_t*>(ex_s + (c & 15) * 256 + 128)[lane];
+            const int there = (int)w.s.len - k0 - 4 * lane;
+            uint32_t b4 = e4 & ~__vcmpeq4(e4, 0xffffffffu);
+            b4 &= there <= 0 ? 0u : there >= 4 ? 0xffffffffu : (1u << (8 * there)) - 1;
+            b4 = __vmaxu4(b4, b4 >> 16);
+            const int top = (int)__reduce_max_sync(0xffffffffu, __vmaxu4(b4, b4 >> 8) & 0xff);
+            cv = top <= 7 ? 0 : top - 127;
+          }
+          const int dt = ve - cv, d = min(max(dt, kDvMin), kDvMax);
+          dv = (float)d;
+          pe = exp2i(-d);
+          pv = ve == kNoRow ? 1.f : exp2i(min(max(dt - d, -126), 0));
+        }
         if (masked) {
           live = t < w.s.len && ((ok >> (r >> shift)) & 1u);
           // (a barrier's parity tells a phase only from the one before it: with
@@ -448,7 +452,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
             y[n] = live && t >= fl.x && t <= fl.y ? y[n] : -INFINITY;
           }
         }
-        bool grow = j == j0 || !go || (Q8 && live && ve > cv + kDvMax);
+        bool grow = j == j0 || !go;
         const float tau = kTau - dv;
 #pragma unroll
         for (int n = 0; n < RQ; n += 4) {
@@ -458,32 +462,6 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         if (bar_red_or(bar_or, 128, grow)) {
           go = !bar_red_or(bar_or, 128, !go);
           if (!go) break;
-          int up = 0;  // what cv grows by
-          if constexpr (Q8) {
-            const int top = __reduce_max_sync(0xffffffffu, live ? ve : kNoRow);
-            if (lane == 0) top_s[half * 4 + q4] = top;
-            bar_named_sync(bar_wg, 128);
-            const int x = max(max(top_s[half * 4], top_s[half * 4 + 1]), max(top_s[half * 4 + 2], top_s[half * 4 + 3]));
-            if (j == j0) {
-              cv = cl = x == kNoRow ? 0 : x;
-            } else if (x > cv + kDvMax) {
-              up = x - cv;
-              cv = x;
-              float most = 0.f;
-#pragma unroll
-              for (int n = 0; n < RQ; ++n) most = fmaxf(most, l[n]);
-              most = warp_max(most);
-              if (lane == 0) red[q4 * 64 + 63] = most;  // (RQ is at most 32)
-              bar_named_sync(bar_wg, 128);
-              most = fmaxf(fmaxf(red[63], red[127]), fmaxf(red[191], red[255]));
-              // (sums of up to 2^67; none yet: any power will do)
-              const int k = most > 0.f ? min(max(kSumMax + 127 - (int)(__float_as_uint(most) >> 23), 0), min(up, 127)) : up;
-              cl += k;
-#pragma unroll
-              for (int n = 0; n < RQ; ++n) l[n] *= exp2i(min(k, 127));
-            }
-            relative();
-          }
           // new maxima: over the warp's keys, then over the four warps (the
           // sums of tile c - 2 are complete: waited for above)
 #pragma unroll
@@ -499,7 +477,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
             for (int n = 0; n < 8; ++n) {
               const int q = n0 + n;
               const float x = fmaxf(fmaxf(red[q], red[64 + q]), fmaxf(red[128 + q], red[192 + q]));
-              const float m = mine_m[q] - (float)up;
+              const float m = mine_m[q];
               f[n] = x > m ? (m == -INFINITY ? 0.f : ex2_approx(m - x)) : 1.f;
               l[q] *= f[n];
             }
@@ -513,7 +491,7 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
           }
           bar_named_sync(bar_wg, 128);  // every thread has read the old maxima
           if (r < RQ)
-            mine_m[r] = fmaxf(fmaxf(fmaxf(red[r], red[64 + r]), fmaxf(red[128 + r], red[192 + r])), mine_m[r] - (float)up);
+            mine_m[r] = fmaxf(fmaxf(fmaxf(red[r], red[64 + r]), fmaxf(red[128 + r], red[192 + r])), mine_m[r]);
           bar_named_sync(bar_wg, 128);
         }
         // weights
@@ -547,10 +525,10 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         if (lane == n % 32) red[q4 * 64 + n] = x;
       }
       bar_named_sync(bar_wg, 128);
-      // 8-bit: the sums are in units of 2^(m - kUp + cv - cl), O^T of 2^(m - kUp + cv)
-      const float dm = Q8 ? kUp - (float)(cv - cl) : 0.f;
+      // 8-bit: the sums are in units of 2^(m - kUp), O^T of 2^(m - kUp + cv)
+      const float dm = Q8 ? kUp : 0.f;
       float2* fin_s = reinterpret_cast<float2*>(sm + S::off_fin);
-      const float up = Q8 ? exp2i(cl) : 1.f;
+      const float up = Q8 ? exp2i(cv) : 1.f;
       if (half == 1) {
         if (r < RQ)
           fin_s[r] = make_float2(mine_m[r] - dm, (red[r] + red[64 + r]) + (red[128 + r] + red[192 + r]));

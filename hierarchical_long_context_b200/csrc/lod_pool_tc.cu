@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
   pdl_wait();               // (the plan)
-  clear_refused<__nv_bfloat16, D>(a, a.Wb);
+  clear_refused<__nv_bfloat16, D, true>(a, a.Wb);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

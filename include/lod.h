@@ -509,7 +509,7 @@ int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, s
  * With bits = 8 and more than 32 query rows (max_new * Hq/Hkv), a key or value
  * row is taken relative to the largest row of its 128 tokens and loses
  * precision when it is smaller than 2^-14 of it.  With bits = 8 value rows
- * smaller than 2^-60 of the sequence's largest lose precision.
+ * (those of zeros aside) that lie more than 2^60 apart lose precision.
  * Keys in a bad block are left out; a row that sees no key then, and every
  * row of a refused sequence that lies in [0, N) and belongs to no other, gets
  * out = 0 and lse = -inf.
