@@ -3,6 +3,7 @@
 // pool's read-back into a dense cache.
 #include <cuda_fp8.h>
 
+#include "lod_host.cuh"
 #include "lod_pool.cuh"
 
 namespace lod {
@@ -34,30 +35,33 @@ __device__ __forceinline__ bool rises(const BatchView& bt, int b) {
 }
 
 // Sequence that owns packed row n, -1: none.  It begins at or below n, at or
-// above every earlier entry, and is the first that ends behind n.  Found by the warp
-// 32 probes at a time as the largest b with begin[b] <= n, which is that one
-// while new_begin rises; else by looking at all.
-__device__ __forceinline__ int owner(const BatchView& bt, int64_t n) {
+// above every earlier entry, and is the first that ends behind n.  Where
+// new_begin does not fall (`falls`, of the whole batch) that is the largest b
+// with begin[b] <= n, which the warp finds 32 probes at a time; where it does,
+// all are looked at.
+__device__ __forceinline__ int owner(const BatchView& bt, int64_t n, bool falls) {
   const int lane = threadIdx.x & 31;
+  if (falls) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < bt.B; b0 += 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < bt.B && bt.begin[b0 + lane + 1] > n);
+      if (m == 0) continue;
+      const int b = b0 + __ffs(m) - 1;
+      return bt.begin[b] <= n && rises(bt, b) ? b : -1;
+    }
+    return -1;
+  }
   int lo = 0, hi = bt.B;  // the answer is in [lo, hi)
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int p = lo + lane * step;
     const unsigned m = __ballot_sync(0xffffffffu, p < hi && bt.begin[p] <= n);
-    if (m == 0) return -1;  // (n < begin[0])
+    if (m == 0) return -1;
     const int top = 31 - __clz(m);
     lo += top * step;
     hi = min(hi, lo + step);
   }
-  if (bt.begin[lo] <= n && n < bt.begin[lo + 1] && rises(bt, lo)) return lo;
-#pragma unroll 1
-  for (int b0 = 0; b0 < bt.B; b0 += 32) {
-    const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < bt.B && bt.begin[b0 + lane + 1] > n);
-    if (m == 0) continue;
-    const int b = b0 + __ffs(m) - 1;
-    return bt.begin[b] <= n && rises(bt, b) ? b : -1;
-  }
-  return -1;
+  return bt.begin[lo] <= n && n < bt.begin[lo + 1] ? lo : -1;
 }
 
 enum Sink { kDense = 0, kPoolRaw = 1, kPoolE4m3 = 2 };
@@ -100,6 +104,34 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
   return e + 127;
 }
 
+// Where a token of the call comes from and goes to; ok = false: nowhere.
+struct Place {
+  int64_t b, t, pos, blk;  // sequence and token of its strides, position, block
+  bool ok, store;          // store = false: a bad block, only q_out is written
+};
+template <int SINK>
+__device__ __forceinline__ Place locate(const AppendArgs& a, int64_t n, bool falls) {
+  Place p = {0, n, 0, 0, false, true};
+  if (n >= a.N) return p;
+  if constexpr (SINK == kDense) {
+    p.b = n / a.n_new;
+    p.t = n % a.n_new;
+    const int64_t len = a.seq_lens[p.b];
+    p.ok = len >= a.n_new && len <= a.Tmax;
+    p.pos = len - a.n_new + p.t;
+  } else {
+    const int ob = owner(a.batch, n, falls);
+    if (ob < 0) return p;
+    const SeqView s = seq_view(a.batch, a.pool.shift, ob);
+    if (!s.ok) return p;
+    p.ok = true;
+    p.pos = s.len - s.n + (n - s.r0);
+    p.blk = a.batch.table[(int64_t)ob * a.batch.max_blocks + (p.pos >> a.pool.shift)];
+    p.store = p.blk >= 0 && p.blk < a.pool.blocks;
+  }
+  return p;
+}
+
 // One warp per (token, share of its heads); a row of d channels is held by
 // LPR lanes, 16 bytes each, so a pass of the warp covers 32 / LPR rows (heads)
 // of the token, and the next kBatch passes' rows are loaded while those are
@@ -115,47 +147,16 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 // CTAs an SM (223), tokens in a loop over warps that keep their weights (230),
 // one flat loop over the passes of all kinds (258).
 template <typename T, int D, int SINK>
-__global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+__device__ __forceinline__ void append_token(const AppendArgs& a, float2* tab, int64_t job, const Place& p) {
   constexpr int E = 16 / (int)sizeof(T);
   constexpr int LPR = D / E, RPW = 32 / LPR;
   constexpr int kBatch = 2;
-  __shared__ float2 tab[4][kMaxPairs];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR, e0 = li * E;
-
-  if (SINK != kDense && a.status && blockIdx.x == 0) {
-    bool bad = false;
-    for (int b = threadIdx.x; b < a.batch.B; b += blockDim.x) bad |= !seq_view(a.batch, a.pool.shift, b).ok;
-    if (bad) set_status(a.status, LOD_ST_BAD_SEQLEN);
-  }
-  const int64_t job = (int64_t)blockIdx.x * 4 + warp;
-  const int64_t n = job / a.split;
   const int part = (int)(job % a.split);
-  if (n >= a.N) return;
-
-  // where the token goes
-  int64_t b, t, pos, blk = 0;
-  bool store = true;
-  if constexpr (SINK == kDense) {
-    b = n / a.n_new;
-    t = n % a.n_new;
-    const int64_t len = a.seq_lens[b];
-    if (len < a.n_new || len > a.Tmax) return;
-    pos = len - a.n_new + t;
-  } else {
-    const int ob = owner(a.batch, n);
-    if (ob < 0) return;
-    const SeqView s = seq_view(a.batch, a.pool.shift, ob);
-    if (!s.ok) return;
-    b = 0;
-    t = n;
-    pos = s.len - s.n + (n - s.r0);
-    blk = a.batch.table[(int64_t)ob * a.batch.max_blocks + (pos >> a.pool.shift)];
-    if (blk < 0 || blk >= a.pool.blocks) {
-      if (lane == 0) set_status(a.status, LOD_ST_BAD_PAGE);
-      store = false;
-    }
-  }
+  if (SINK != kDense && !p.store && lane == 0) set_status(a.status, LOD_ST_BAD_PAGE);
+  const int64_t b = p.b, t = p.t, pos = p.pos, blk = p.blk;
+  const bool store = p.store;
   const int64_t in_block = pos & (((int64_t)1 << a.pool.shift) - 1);
 
   // the passes of queries, keys and values, and this warp's share of them
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_consta
   const int half = a.use_rope ? a.rope.rot >> 1 : 0, rot = 2 * half;
   const bool inter = a.rope.interleaved != 0;
   if (p0 < pq + pk) {
-    for (int i = lane; i < half; i += 32) tab[warp][i] = turn(pos, a.rope.freq[i]);
+    for (int i = lane; i < half; i += 32) tab[i] = turn(pos, a.rope.freq[i]);
     __syncwarp();
   }
   const bool by_shuffle = !inter && half % E == 0;  // the partner channels sit in one other lane
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_consta
         sw[i] = 0.f;
         if (e < rot) {
           const bool second = inter ? (e & 1) : e >= half;
-          const float2 cs = tab[warp][inter ? e >> 1 : second ? e - half : e];
+          const float2 cs = tab[inter ? e >> 1 : second ? e - half : e];
           const int pe = inter ? e ^ 1 : second ? e - half : e + half;
           cw[i] *= cs.x;
           sw[i] = (second ? cs.y : -cs.y) * (w ? Elem<T>::to_f(w[pe]) : 1.f);
@@ -314,12 +315,72 @@ __global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_consta
   }
 }
 
+// A CTA of a pool's append looks once whether new_begin falls.  Of few
+// sequences every CTA does, for its four warps' one token each, and while it
+// looks for the tokens' sequences as if it did not fall.  Of many (kMany) the
+// grid fits the GPU and the warps take their tokens in turn, as the look costs
+// more than a token (65535 sequences of one token: 182 us without it, 220
+// so, 1140 with a look of every warp; 2048: 19.1, 21.1).
+constexpr int kManySeqs = 1024;
+template <typename T, int D, int SINK, bool kMany>
+__global__ void __launch_bounds__(128, 6) append_rows_kernel(const __grid_constant__ AppendArgs a) {
+  __shared__ float2 tab[4][kMaxPairs];
+  const int warp = threadIdx.x >> 5;
+  int64_t job = (int64_t)blockIdx.x * 4 + warp;
+  bool falls = false;
+  const int64_t* begin = a.batch.begin;
+  const int B = a.batch.B;
+  if constexpr (kMany) {
+#pragma unroll 8
+    for (int i = threadIdx.x + 1; i < B; i += 128) falls |= begin[i] < begin[i - 1];
+    falls = __syncthreads_or(falls);
+    for (; job < a.N * a.split; job += (int64_t)gridDim.x * 4) {
+      const Place p = locate<SINK>(a, job / a.split, falls);
+      if (p.ok) append_token<T, D, SINK>(a, tab[warp], job, p);
+      __syncwarp();  // (tab)
+    }
+  } else {
+    // (the first entries are on their way while the tokens are looked for; up
+    // to 33 a warp looks at by itself, without the CTA's barrier)
+    int64_t x[4], y[4];
+    const int i0 = SINK != kDense && B <= 33 ? threadIdx.x & 31 : threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + 128 * k;
+      x[k] = y[k] = 0;
+      if (SINK != kDense && i + 1 < B) x[k] = begin[i], y[k] = begin[i + 1];
+    }
+    Place p = locate<SINK>(a, job / a.split, false);
+    if constexpr (SINK != kDense) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) falls |= y[k] < x[k];
+#pragma unroll 4
+      for (int i = i0 + 513; i < B; i += 128) falls |= begin[i] < begin[i - 1];
+      falls = B <= 33 ? __any_sync(0xffffffffu, falls) != 0 : __syncthreads_or(falls) != 0;
+      if (falls) p = locate<SINK>(a, job / a.split, true);
+    }
+    if (p.ok) append_token<T, D, SINK>(a, tab[warp], job, p);
+  }
+  if (SINK != kDense && a.status && blockIdx.x == 0) {
+    bool bad = false;
+    for (int b = threadIdx.x; b < B; b += 128) bad |= !seq_view(a.batch, a.pool.shift, b).ok;
+    if (bad) set_status(a.status, LOD_ST_BAD_SEQLEN);
+  }
+}
+
+template <typename T, int D, int SINK>
+cudaError_t launch_append_sink(const AppendArgs& a, int64_t grid, cudaStream_t st) {
+  const int64_t fit = (int64_t)host::num_sms() * 6;
+  if (SINK != kDense && a.batch.B > kManySeqs && grid > fit)
+    append_rows_kernel<T, D, SINK == kDense ? kPoolRaw : SINK, true><<<(unsigned)fit, 128, 0, st>>>(a);
+  else
+    append_rows_kernel<T, D, SINK, false><<<(unsigned)grid, 128, 0, st>>>(a);
+  return cudaGetLastError();
+}
 template <typename T, int D>
 cudaError_t launch_append_t(const AppendArgs& a, int sink, int64_t grid, cudaStream_t st) {
-  if (sink == kDense) append_rows_kernel<T, D, kDense><<<(unsigned)grid, 128, 0, st>>>(a);
-  else if (sink == kPoolRaw) append_rows_kernel<T, D, kPoolRaw><<<(unsigned)grid, 128, 0, st>>>(a);
-  else append_rows_kernel<T, D, kPoolE4m3><<<(unsigned)grid, 128, 0, st>>>(a);
-  return cudaGetLastError();
+  if (sink == kDense) return launch_append_sink<T, D, kDense>(a, grid, st);
+  return sink == kPoolRaw ? launch_append_sink<T, D, kPoolRaw>(a, grid, st) : launch_append_sink<T, D, kPoolE4m3>(a, grid, st);
 }
 
 // ---------------------------------------------------------------- read-back
@@ -439,7 +500,7 @@ cudaError_t launch_append_rows(const AppendArgs& args, int dtype, int d, bool po
   const int elem = dtype == LOD_DTYPE_F32 ? 4 : 2;
   const int rpw = 32 / (d * elem / 16);
   const int passes = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);
-  int64_t split = (int64_t)148 * 16 / a.N;
+  int64_t split = (int64_t)host::num_sms() * 16 / a.N;
   if (split > passes) split = passes;
   if (split < 1) split = 1;
   a.split = (int)split;
