@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
         mma_commit_if(lead, &s_full[2 * s + u]);
         any = true;
       };
-      for (int part = blockIdx.x; part < parts && go; part += a.ctas) {
+      int part = blockIdx.x;
+      for (; part < parts && go; part += a.ctas) {
         Walk<kTM, kKT> w(a, a.Wb, part);
         for (; w.more() && go; w.next()) {
         const int T = w.kt1 - w.kt0;
@@ -239,6 +240,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       }
         if (s == 0 && lane == 0) w.record(part);
       }
+      // (the parts a timed-out CTA leaves: the merge must not take what an
+      // earlier call recorded there, rows of another batch)
+      for (; part < parts && s == 0; part += a.ctas)
+        if (lane == 0) a.rec[part] = {0, 0, 0, 0, 0};
       if (any) {
         mma_commit_if(lead, &fin[s]);
         (void)mbar_wait(&fin[s], 0, a.status);
