@@ -21,6 +21,26 @@ int32_t check_strides(const int64_t* s, int count, int64_t elem, const char* nam
   return LOD_OK;
 }
 
+// The rows of an output lie apart: taken by rising stride, each dimension
+// steps over all that the smaller ones cover (every slice and permutation of a
+// contiguous array does).
+int32_t check_apart(const int64_t* s, const int64_t* sizes, int count, int64_t d, const char* name) {
+  int64_t covered = d, last = -1;
+  int at = -1;
+  for (int k = 0; k < count; ++k) {
+    int next = -1;
+    for (int i = 0; i < count; ++i)
+      if ((s[i] > last || (s[i] == last && i > at)) &&
+          (next < 0 || s[i] < s[next])) next = i;
+    last = s[next], at = next;
+    if (sizes[next] <= 1) continue;
+    if (last < covered || last > (INT64_MAX - covered) / sizes[next])
+      return fail(LOD_EINVAL, "%s gives rows that overlap", name);
+    covered += last * (sizes[next] - 1);
+  }
+  return LOD_OK;
+}
+
 int32_t check_rope(const lod_rope* r, int32_t d) {
   if (!(r->eps >= 0.f)) return fail(LOD_EINVAL, "rope eps must be >= 0");
   if (r->rot < 0 || r->rot > d || (r->rot & 1)) return fail(LOD_EINVAL, "rope rot = %d must be even, in [0, d]", r->rot);
@@ -112,12 +132,14 @@ lod::RopeView rope_view(const lod_rope* r) {
 }
 
 // q and q_out of an append: both or neither, aligned, with `count` strides.
-int32_t check_queries(const void* q, const int64_t* qs, const void* q_out, const int64_t* os, int count, int64_t elem) {
+int32_t check_queries(const void* q, const int64_t* qs, const void* q_out, const int64_t* os, const int64_t* sizes,
+                      int count, int64_t elem, int64_t d) {
   if (!q != !q_out) return fail(LOD_EINVAL, "q and q_out go together");
   if (!q) return LOD_OK;
   if (!aligned16(q) || !aligned16(q_out)) return fail(LOD_EINVAL, "q and q_out must be 16-byte aligned");
   int32_t rc = check_strides(qs, count, elem, "q_strides");
   if (!rc) rc = check_strides(os, count, elem, "q_out_strides");
+  if (!rc) rc = check_apart(os, sizes, count, d, "q_out_strides");
   if (!rc && q == q_out)
     for (int i = 0; i < count; ++i)
       if (qs[i] != os[i]) return fail(LOD_EINVAL, "q_out may be q itself only with the strides of q");
@@ -160,7 +182,8 @@ int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q
   const int64_t N = p->B * n_new;
   if (N >= ((int64_t)1 << 31)) return fail(LOD_EUNSUPPORTED, "B * n_new must stay below 2^31");
   rc = check_rope(rope, p->d);
-  if (!rc) rc = check_queries(q, q_strides, q_out, q_out_strides, 3, elem);
+  const int64_t rows[3] = {p->B, p->Hq, n_new};
+  if (!rc) rc = check_queries(q, q_strides, q_out, q_out_strides, rows, 3, elem, p->d);
   if (!rc) rc = check_new_kv(k, v, kv_new_strides, 3, elem);
   if (!rc) rc = check_visible_all({{seq_lens, "seq_lens"}, {K, "K"}, {V, "V"}});
   if (rc) return rc;
@@ -199,7 +222,8 @@ int32_t lod_pool_append(const lod_pool* pool, const lod_batch* batch, const lod_
   const int64_t elem = elem_of(pool->dtype);
   if (q && !rope) return fail(LOD_EINVAL, "q without rope: the queries would only be copied");
   if (rope) rc = check_rope(rope, pool->d);
-  if (!rc) rc = check_queries(q, q_strides, q_out, q_out_strides, 2, elem);
+  const int64_t rows[2] = {batch->N, pool->Hq};
+  if (!rc) rc = check_queries(q, q_strides, q_out, q_out_strides, rows, 2, elem, pool->d);
   if (!rc) rc = check_new_kv(k, v, kv_new_strides, 2, elem);
   if (!rc) rc = check_status(status);
   if (rc) return rc;
@@ -238,6 +262,8 @@ int32_t lod_pool_read(const lod_pool* pool, const lod_batch* batch, int64_t t_be
   if (!aligned16(K) || !aligned16(V)) return fail(LOD_EINVAL, "K and V must be 16-byte aligned");
   rc = check_strides(kv_strides, 3, elem_of(pool->dtype), "kv_strides");
   if (!rc && kv_strides[2] < pool->d) rc = fail(LOD_EINVAL, "token stride smaller than d");
+  const int64_t rows[3] = {batch->B, pool->Hkv, t_end};
+  if (!rc) rc = check_apart(kv_strides, rows, 3, pool->d, "kv_strides");
   if (!rc) rc = check_visible_all({{K, "K"}, {V, "V"}});
   if (!rc) rc = check_status(status);
   if (rc) return rc;
@@ -277,6 +303,8 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
   if (reinterpret_cast<uintptr_t>(lse) & 3u) return fail(LOD_EINVAL, "lse must be 4-byte aligned");
   rc = check_strides(q_strides, 2, elem, "q_strides");
   if (!rc) rc = check_strides(out_strides, 2, elem, "out_strides");
+  const int64_t rows[2] = {batch->N, pool->Hq};
+  if (!rc) rc = check_apart(out_strides, rows, 2, pool->d, "out_strides");
   if (rc) return rc;
   if (window < 0) return fail(LOD_EINVAL, "window = %lld must be >= 0 (0: none)", (long long)window);
   if (!(scale <= 0.f) && !std::isfinite(scale)) return fail(LOD_EINVAL, "scale must be finite");

@@ -389,7 +389,8 @@ typedef struct lod_rope {
  *            itself (same strides).  q and q_out are both NULL to append k
  *            and v alone.
  * Innermost channels are contiguous; pointers and strides are 16-byte
- * aligned.  The buffers above may be page-locked host memory.  A sequence
+ * aligned, and strides that make rows of an output overlap are refused (here
+ * and in the calls below).  The buffers above may be page-locked host memory.  A sequence
  * whose length is below n_new or above Tmax is skipped (cache and q_out left
  * as they were).
  */

@@ -148,3 +148,20 @@ def test_a_window_as_long_as_any_is_no_window():
     want = lod.lod_pool_attend(pool, batch, q)
     for window in (L, 1 << 40, (1 << 63) - n, (1 << 63) - 1):
         assert torch.equal(lod.lod_pool_attend(pool, batch, q, window=window), want), window
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    g = gen(105)
+    pool, table = make_pool(g, [50, 60], 16, 4, 2, 64, BF, 0)
+    batch = api.PoolBatch(table, torch.tensor([50, 60], device="cuda"), torch.tensor([0, 2, 5], device="cuda"), tokens=5,
+                          max_new=3)
+    q, k = randn(g, 5, 4, 64, dtype=BF), randn(g, 5, 2, 64, dtype=BF)
+    one = torch.zeros(1, 4, 64, dtype=BF, device="cuda")
+    for bad in (one.expand(5, 4, 64), torch.zeros(5, 1, 64, dtype=BF, device="cuda").expand(5, 4, 64)):
+        with pytest.raises(lod.LodError, match="overlap"):
+            lod.lod_pool_attend(pool, batch, q, out=bad)
+        with pytest.raises(lod.LodError, match="overlap"):
+            lod.lod_pool_append(pool, batch, k, k, rope=api.Rope(), q=q, q_out=bad)
+    row = torch.zeros(1, 2, 64, 64, dtype=BF, device="cuda").expand(2, 2, 64, 64)
+    with pytest.raises(lod.LodError, match="overlap"):
+        lod.lod_pool_read(pool, batch, row, row)

@@ -6,7 +6,7 @@ import torch
 
 import hierarchical_long_context_b200 as lod
 from hierarchical_long_context_b200 import _lib, api
-from tests.test_pool_refusals import FAKE, _append, _cpu_batch, _cpu_pool, err
+from tests.test_pool_refusals import FAKE, _append, _cpu_batch, _cpu_pool, err, s3
 
 
 def _dense(B=3, T=256):
@@ -55,3 +55,24 @@ def test_a_pool_and_a_rope_are_fixed():
             setattr(obj, name, None)
     r.ref(64, torch.bfloat16)
     r.ref(128, torch.float32)
+
+
+@pytest.mark.parametrize("os, good", [
+    (s3(4096 * 16, 128, 16 * 128), True),              # [b][token][head]
+    (s3(128, 256, 4096), True),                        # [token][head][b], B = 2 and 16 heads
+    (s3(1 << 60, 128, 2048), True),
+    (s3(0, 128, 2048), False), (s3(1 << 20, 0, 128), False), (s3(1 << 20, 128, 0), False),
+    (s3(1 << 20, 64, 2048), False),                    # heads closer than a row
+    (s3(1 << 20, 128, 1024), False),                   # a token's 16 heads reach into the next token
+    (s3(2048, 128, 2048), False),
+    (s3(1 << 62, 1 << 62, 1 << 62), False),
+])
+def test_outputs_whose_rows_overlap_are_refused(os, good):
+    """2 sequences of 3 tokens, 16 heads of 128 channels.  (Good strides get as far as the made-up addresses.)"""
+    rc = _append(q=FAKE, qo=FAKE + 4096, qs=s3(), os=os, n=3)
+    assert rc == _lib.LOD_EINVAL and ("overlap" in err()) != good, err()
+
+
+def test_single_rows_may_have_any_stride():
+    p = lod.Params(B=1, Hq=1, Hkv=1, d=128, Tmax=4096).c()
+    assert _append(p=p, q=FAKE, qo=FAKE + 4096, qs=s3(), os=s3(0, 0, 0), n=1) == _lib.LOD_EINVAL and "overlap" not in err()
