@@ -141,9 +141,10 @@ __device__ __forceinline__ Place locate(const AppendArgs& a, int64_t n, bool fal
 // row takes out = rstd * (x * cw + partner * sw): the partners cross lanes as
 // the stored 16-byte words, not as floats.  Every row is read once and written
 // once.  32768 tokens of 32 + 16 heads, 128 bf16 channels (805 MB in and out):
-// 207 us, 59 % of the measured copy rate; without norm and rotation 178 us,
+// 213 us, 58 % of the measured copy rate; without norm and rotation 178 us,
 // so the issue of about 75 instructions a pass and the latency at a token's
-// start bound it, not the bytes.  Measured and dropped: batches of 4 (220), 8
+// start bound it, not the bytes (the six CTAs an SM cost up to 80 bytes of
+// spills a thread in the bf16 forms).  Measured and dropped: batches of 4 (220), 8
 // CTAs an SM (223), tokens in a loop over warps that keep their weights (230),
 // one flat loop over the passes of all kinds (258).
 template <typename T, int D, int SINK>

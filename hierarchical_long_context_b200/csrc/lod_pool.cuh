@@ -97,14 +97,13 @@ struct PoolAttendArgs {
   float2* ml;              // [parts][2][TM] their (max, sum), log2 units
   struct MergeRec* rec;    // [parts] the unit that opens in a part and goes on behind it
   int ctas;
-  int min_share;           // key tiles a CTA takes at least
   int planned;             // 1: Wb, RT, pre were written by the plan kernel
   // The kernel of many rows takes the list in rounds: a CTA's parts are c, c +
   // ctas, ... of ctas * rounds.  The CTAs of a round then read about
   // kRoundBytes of the cache between them, which stays in L2 while the
   // row tiles of a head sweep over it at offsets of their own (a 2048-token
   // chunk over 128K read 15.8 GB from DRAM in one round, for 0.54 GB of cache;
-  // rounds of 64 MB take 4.21 ms, of 96 MB 4.49, of 40 MB 4.41).
+  // rounds of 64 MB take 4.31 ms, of 96 MB 4.55, of 40 MB 4.31).
   int max_rounds;
   int32_t* rounds;         // (null: one round)
   int row_bytes;           // stored bytes of a key and its value
@@ -213,8 +212,7 @@ struct __align__(16) MergeRec {
 __device__ __forceinline__ int list_parts(const PoolAttendArgs& a) { return a.ctas * (a.rounds ? *a.rounds : 1); }
 __device__ __forceinline__ int64_t list_share(const PoolAttendArgs& a, int64_t total) {
   const int parts = list_parts(a);
-  const int64_t s = (total + parts - 1) / parts;
-  return s > a.min_share ? s : a.min_share;
+  return (total + parts - 1) / parts;
 }
 
 // A CTA's walk through a part [w, w1) of the list, one piece of a unit at a

@@ -341,7 +341,6 @@ int32_t lod_pool_attend(const lod_pool* pool, const lod_batch* batch, const void
   a.ctas = s.ctas;
   a.max_rounds = s.max_rounds;
   a.row_bytes = lod::pool_row_bytes(pool->dtype, pool->bits, pool->d);
-  a.min_share = 1;
   lod::PoolMaps maps;
   const bool tma = s.kind != 0 && pool->bits == 0;
   if (tma) {

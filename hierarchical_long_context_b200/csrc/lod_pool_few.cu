@@ -12,7 +12,7 @@ struct FewSmem {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kWide = D == 64 ? 2 : 1;  // d = 64 has room for twice the stages
   // stages: what 227 KB hold beside the query and weight tiles.  (8-bit, at
-  // most 16 rows: two bf16 tiles of each kind and two of codes, not one and
+  // most 16 rows: two f16 tiles of each kind and two of codes, not one and
   // three: with one the conversion of a tile waits for the MMAs of the last)
   static constexpr int KS = kWide * (Q8 ? (RQ <= 16 ? 2 : 1) : RQ == 64 ? 2 : 3);
   static constexpr int VS = kWide * (Q8 ? 2 : RQ >= 32 ? 2 : 3);
@@ -68,11 +68,11 @@ struct FewSmem {
 // end), with an 8-bit pool warps 12-15 and 16-19 codes to f16 (keys, values).
 // Bounds: the cache's bytes, 64 KB a tile (bf16, d = 128) at 1/148 of the HBM
 // rate, 1.5 us; the tensor work is below a tenth of that.  Measured at 4 x 64K
-// tokens, 64 / 8 heads, one new token: bf16 169 us (6.36 TB/s, 97 % of the
-// measured copy rate), d = 64 100 us (5.37 TB/s), four new tokens 198 us.
-// 8-bit: 140 us (3.8 TB/s).  There the codes and f16 tiles that go in and out
+// tokens, 64 / 8 heads, one new token: bf16 168 us (6.38 TB/s, 97 % of the
+// measured copy rate), d = 64 95 us (5.63 TB/s), four new tokens 195 us.
+// 8-bit: 130 us (4.15 TB/s).  There the codes and f16 tiles that go in and out
 // of shared memory, 192 KB a tile, take 1500 cycles of it (the load and store
-// instructions' part reads 31 % of that pipe), against 1400 for the bytes from
+// instructions' part reads 32 % of that pipe), against 1400 for the bytes from
 // HBM, and the conversion and softmax chains share the rest.
 template <int D, int RQ, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)

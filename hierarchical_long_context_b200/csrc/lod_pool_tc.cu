@@ -48,7 +48,7 @@ struct RowsSmem {
 // Bounds, per 128 keys and 256 rows: 2048 cycles of tensor work (d = 128; 2560
 // with the scores' MMAs of 64 keys, which read their queries twice as often),
 // 2048 of exponentials on the special-function unit alone (16 a clock).
-// Measured: 2048 new tokens over 128K, 32 / 8 heads, 4.36 ms (1.0 PFLOP/s) in a
+// Measured: 2048 new tokens over 128K, 32 / 8 heads, 4.30 ms (1.0 PFLOP/s) in a
 // loop, where the power cap holds the clock at 1.45 GHz, 3.8 ms before it does.
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       go = !bar_red_or(1 + s, 128, !go);
     }
   } else if constexpr (Q8) {
-    // ============================================================== codes to bf16 tiles
+    // ============================================================== codes to f16 tiles
     regs_dec<80>();
     int c = 0;
     bool go = true;

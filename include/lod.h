@@ -487,8 +487,9 @@ int32_t lod_pool_read(const lod_pool* pool, const lod_batch* batch, int64_t t_be
  * Workspace bytes of lod_pool_attend for a batch of exactly these B,
  * max_blocks, N and max_new (device pointers of pool and batch are not looked
  * at; a larger workspace serves as well, and one of the largest of several
- * calls serves them all).  256-byte aligned device memory,
- * zeroed once after allocation; its first word is the status word of
+ * calls serves them all, one after another: calls whose executions can overlap,
+ * on two streams or as two graphs, need one each).  256-byte aligned device
+ * memory, zeroed once after allocation; its first word is the status word of
  * lod_get_status.
  */
 int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, size_t* bytes);
