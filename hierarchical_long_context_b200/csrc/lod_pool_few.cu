@@ -403,11 +403,12 @@ __global__ void __launch_bounds__(Q8 ? 640 : 384, 1)
         if constexpr (Q8) {
           if (j == j0) {
             // cv, by each warp from the tile's bytes: four a lane, those of
-            // NaN rows and behind the length left out
+            // NaN rows, behind the length and before every window left out
             const uint32_t e4 = reinterpret_cast<const uint32_t*>(ex_s + (c & 15) * 256 + 128)[lane];
-            const int there = (int)w.s.len - k0 - 4 * lane;
+            const int there = (int)w.s.len - k0 - 4 * lane, before = first_lo - k0 - 4 * lane;
             uint32_t b4 = e4 & ~__vcmpeq4(e4, 0xffffffffu);
             b4 &= there <= 0 ? 0u : there >= 4 ? 0xffffffffu : (1u << (8 * there)) - 1;
+            b4 &= before <= 0 ? 0xffffffffu : before >= 4 ? 0u : 0xffffffffu << (8 * before);
             b4 = __vmaxu4(b4, b4 >> 16);
             const int top = (int)__reduce_max_sync(0xffffffffu, __vmaxu4(b4, b4 >> 8) & 0xff);
             cv = top <= 7 ? 0 : top - 127;

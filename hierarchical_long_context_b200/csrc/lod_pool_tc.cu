@@ -255,15 +255,21 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1)
       bool go = true;
       for (int part = blockIdx.x; part < parts && go; part += a.ctas)
       for (Walk<kTM, kKT> w(a, a.Wb, part); w.more() && go; w.next()) {
+        // (of the keys that some row of the unit sees: what else the tile holds
+        // is masked, and cleared where it is values)
+        const int p0 = (int)(w.s.len - w.s.n), last_unit = p0 + ((int)w.u.i * kTM + w.nrow - 1) / a.G;
+        const int64_t first_unit = a.window > 0 ? p0 + (int)w.u.i * kTM / a.G - a.window + 1 : 0;
         for (int kt = w.kt0; kt < w.kt1 && go; ++kt, ++t) {
           for (int kv = 0; kv < 2; ++kv) {
             if (!(go = __all_sync(0xffffffffu, wait(&raw_full[kv], (uint32_t)t & 1u)))) break;
             unsigned char* ex = sm + S::off_raw + kv * S::kRaw + 128 * D;
             const uint32_t e4 = reinterpret_cast<const uint32_t*>(ex)[lane];
-            const int n = (int)w.s.len - kt * kKT - 4 * lane;  // tokens of this lane's four
+            const int n = last_unit + 1 - kt * kKT - 4 * lane;  // tokens of this lane's four
+            const int before = first_unit > 0 ? (int)first_unit - kt * kKT - 4 * lane : 0;
             const bool there = (info_s[32 + kv * 16 + (t & 15)] >> (4 * lane >> shift)) & 1;
             uint32_t live = e4 & ~__vcmpeq4(e4, 0xffffffffu);  // (a row of NaN does not count)
             live &= !there || n <= 0 ? 0u : n >= 4 ? 0xffffffffu : (1u << (8 * n)) - 1;
+            live &= before <= 0 ? 0xffffffffu : before >= 4 ? 0u : 0xffffffffu << (8 * before);
             uint32_t m = __vmaxu4(live, live >> 16);
             m = __vmaxu4(m, m >> 8) & 0xff;
             const int top = (int)__reduce_max_sync(0xffffffffu, m);

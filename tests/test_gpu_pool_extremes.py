@@ -165,6 +165,42 @@ def test_tiles_of_small_values_beside_tiles_of_large_ones(small, large, low, ord
     check(pool, table, [L], [n], unit_queries(n, Hq, d, dtype), 1.0)
 
 
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
+@pytest.mark.parametrize("n", [1, 4, 60])
+def test_huge_rows_that_no_query_sees_cost_nothing(n, dtype, bits):
+    """The tile in which the window begins also holds rows before it, 2^90 times as large."""
+    g = gen(206)
+    L, Hq, Hkv, d, window = 1000, 8, 2, 64, 300
+    k, v = randn(g, L, Hkv, d), randn(g, L, Hkv, d)
+    k[L - n - window - 20:L - n - window - 10] *= 2.0 ** 90
+    v[L - n - window - 20:L - n - window - 10] *= 2.0 ** 90
+    pool, table = pool_of([(k, v)], 32, Hq, dtype, bits, g)
+    q = randn(g, n, Hq, d, dtype=dtype)
+    begin, out, lse, status = attend(pool, table, [L], [n], q, window=window)
+    assert status == 0
+    o, z, to, tz = pt.attend64(pool, table, [L], begin, q, window)
+    assert o.abs().max() < 10
+    close(lse, z, tz, "lse")
+    close(out, o, to, "out")
+
+
+@pytest.mark.parametrize("dtype, bits", [(BF, 8), (BF, 0), (F32, 8)])
+def test_huge_rows_of_later_tokens_cost_earlier_ones_nothing(dtype, bits):
+    """Two tokens, 8 apart in one key tile, of 64 heads a KV head: the later one's rows are 2^90 times as large."""
+    g = gen(207)
+    L, Hq, Hkv, d, n = 128 * 6, 64, 1, 64, 12
+    k, v = randn(g, L, Hkv, d), randn(g, L, Hkv, d)
+    k[-4:] *= 2.0 ** 90
+    v[-4:] *= 2.0 ** 90
+    pool, table = pool_of([(k, v)], 32, Hq, dtype, bits, g)
+    q = randn(g, n, Hq, d, dtype=dtype)
+    begin, out, lse, status = attend(pool, table, [L], [n], q)
+    o, z, to, tz = pt.attend64(pool, table, [L], begin, q)
+    assert status == 0 and o[:4].abs().max() < 10
+    close(lse[:4], z[:4], tz[:4], "lse")
+    close(out[:4], o[:4], to[:4], "out")
+
+
 # ------------------------------------------------------------------ NaN behind a query
 
 @pytest.mark.parametrize("dtype, bits", [(BF, 0), (BF, 8), (F32, 0), (F32, 8)])
