@@ -185,6 +185,8 @@ int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q
   const int64_t rows[3] = {p->B, p->Hq, n_new};
   if (!rc) rc = check_queries(q, q_strides, q_out, q_out_strides, rows, 3, elem, p->d);
   if (!rc) rc = check_new_kv(k, v, kv_new_strides, 3, elem);
+  const int64_t cached[3] = {p->B, p->Hkv, p->Tmax};
+  if (!rc) rc = check_apart(kv_strides, cached, 3, p->d, "kv_strides");
   if (!rc) rc = check_visible_all({{seq_lens, "seq_lens"}, {K, "K"}, {V, "V"}});
   if (rc) return rc;
   lod::AppendArgs a;

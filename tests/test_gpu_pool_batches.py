@@ -8,7 +8,7 @@ import torch
 import hierarchical_long_context_b200 as lod
 from hierarchical_long_context_b200 import api
 from tests import pooltest as pt
-from tests.test_gpu_pool import BF, F32, ST, close, gen, make_pool, randn
+from tests.test_gpu_pool import BF, F32, ST, close, gen, make_pool, make_rope, randn, rope_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -165,3 +165,43 @@ def test_outputs_whose_rows_overlap_are_refused():
     row = torch.zeros(1, 2, 64, 64, dtype=BF, device="cuda").expand(2, 2, 64, 64)
     with pytest.raises(lod.LodError, match="overlap"):
         lod.lod_pool_read(pool, batch, row, row)
+    p = lod.Params(B=2, Hq=4, Hkv=2, d=64, Tmax=256, dtype=BF)
+    cache = torch.zeros(1, 2, 256, 64, dtype=BF, device="cuda").expand(2, 2, 256, 64)
+    k1 = randn(g, 2, 2, 3, 64, dtype=BF)
+    with pytest.raises(lod.LodError, match="overlap"):
+        lod.lod_append_rope(p, api.Rope(), None, k1, k1, cache, cache, torch.tensor([9, 9], device="cuda"))
+
+
+# ------------------------------------------------------------------ long prompts of fp32
+
+@pytest.mark.parametrize("bits", [0, 8])
+@pytest.mark.parametrize("Hq, Hkv, d, block, rot, inter", [(6, 2, 128, 64, 64, False), (4, 1, 64, 16, 64, True),
+                                                           (8, 8, 128, 128, 24, False)])
+def test_long_fp32_prompts(Hq, Hkv, d, block, rot, inter, bits):
+    """Appends of thousands of fp32 tokens: more than the GPU holds warps for, into fp32 and 8-bit rows."""
+    g = gen(106)
+    lens, new = [6100, 3000, 5], [5000, 2999, 0]
+    pool, table = make_pool(g, lens, block, Hq, Hkv, d, F32, bits)
+    begin = [0, 5000, 7999, 7999]
+    batch = api.PoolBatch(table, torch.tensor(lens, device="cuda"), torch.tensor(begin, device="cuda"), tokens=7999,
+                          max_new=5000)
+    rope, w = make_rope(g, d, F32, rot, inter, True)
+    q, k, v = randn(g, 7999, Hq + 2 * Hkv, d).split([Hq, Hkv, Hkv], 1)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = lod.lod_pool_append(pool, batch, k, v, rope=rope, q=q, status=status)
+    assert int(status) == 0
+    for b in range(2):
+        L, n = lens[b], new[b]
+        rows, pos = slice(begin[b], begin[b + 1]), torch.arange(L - n, L, device="cuda")
+        y, mag = pt.rotate64(q[rows].transpose(0, 1), w[0], pos, rope.inv_freq, inter, 1e-5)
+        close(out[rows].transpose(0, 1), y, rope_tol(y, mag, F32), "q")
+        y, mag = (x.transpose(0, 1) for x in pt.rotate64(k[rows].transpose(0, 1), w[1], pos, rope.inv_freq, inter, 1e-5))
+        rk, rv = pt.pool_rows(pool, table[b], pos)
+        if bits:  # (as the small prompts: nearest codes of values within 2^-19 of the pair's size)
+            e = pt.exponent64(y.float()).double()
+            close(rk, y, 2.0 ** -4 * y.abs() + torch.exp2(e - 9)[..., None] + 2.0 ** -18 * mag, "K")
+            c, ev = pt.quantise64(v[rows])
+            assert torch.equal(rv, pt.codes_to_float(c) * torch.exp2(ev.double() - 127)[..., None])
+        else:
+            close(rk, y, rope_tol(y, mag, F32), "K")
+            assert torch.equal(rv, v[rows].double())
