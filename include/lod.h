@@ -390,9 +390,9 @@ typedef struct lod_rope {
  *            and v alone.
  * Innermost channels are contiguous; pointers and strides are 16-byte
  * aligned, and strides that make rows of an output overlap are refused (here
- * and in the calls below).  The buffers above may be page-locked host memory.  A sequence
- * whose length is below n_new or above Tmax is skipped (cache and q_out left
- * as they were).
+ * and in the calls below).  The buffers above may be page-locked host memory.
+ * A sequence whose length is below n_new or above Tmax is skipped (cache and
+ * q_out left as they were).
  */
 int32_t lod_append_rope(const lod_params* p, const lod_rope* rope, const void* q, const int64_t q_strides[3],
                         const void* k, const void* v, const int64_t kv_new_strides[3], int64_t n_new, void* K,
@@ -511,7 +511,8 @@ int32_t lod_pool_workspace_bytes(const lod_pool* pool, const lod_batch* batch, s
  * With bits = 8 and more than 32 query rows (max_new * Hq/Hkv), a key or value
  * row is taken relative to the largest row of its 128 tokens and loses
  * precision when it is smaller than 2^-14 of it.  With bits = 8 value rows
- * (those of zeros aside) that lie more than 2^60 apart lose precision.
+ * (those of zeros aside) that lie more than 2^60 apart, or are smaller than
+ * 2^-60, lose precision.
  * Keys in a bad block are left out; a row that sees no key then, and every
  * row of a refused sequence that lies in [0, N) and belongs to no other, gets
  * out = 0 and lse = -inf.
